@@ -347,6 +347,189 @@ tq_status tq_decode_step_workspace_size(const tq_params* kp, const tq_params* vp
                                         int Hq, int Hkv, int64_t pos, size_t* bytes);
 
 /*
+ * tq_rope_create -- describe one rotary position embedding.  Pair i of the
+ * rotated part of a head turns by the angle pos * f_i, with
+ *   f_i = base^(-2 i / rot), i < rot / 2,
+ * changed by the scaling:
+ *   TQ_ROPE_PLAIN   f_i
+ *   TQ_ROPE_LINEAR  f_i / factor (positions compressed by factor)
+ *   TQ_ROPE_BANDS   by the turns t_i = orig_len f_i / (2 pi) that a pair makes
+ *                   over the original length: f_i where t_i >= high, f_i /
+ *                   factor where t_i <= low, and between them linear in t_i
+ *   TQ_ROPE_YARN    f_i where the pair makes more than `high` turns over
+ *                   orig_len, f_i / factor where fewer than `low`, linear in
+ *                   the pair's number between (the borders rounded outwards);
+ *                   the rotated part is multiplied by 0.1 ln(factor) + 1
+ *   rot          coordinates of a head that rotate: even, 2..256 (the first
+ *                ones; the others pass)
+ *   interleaved  0: pair i is coordinates (i, i + rot / 2); 1: (2 i, 2 i + 1)
+ *   base         > 1
+ *   factor       >= 1, orig_len > 0, high > low > 0: read by the scalings that
+ *                name them
+ * Host memory only: a handle may be used on every device.
+ */
+typedef enum { TQ_ROPE_PLAIN = 0, TQ_ROPE_LINEAR = 1, TQ_ROPE_BANDS = 2, TQ_ROPE_YARN = 3 } tq_rope_scaling;
+typedef struct tq_rope tq_rope; /* opaque rotary description */
+tq_status tq_rope_create(int rot, int interleaved, double base, tq_rope_scaling scaling,
+                         double factor, double orig_len, double low, double high, tq_rope** out);
+tq_status tq_rope_destroy(tq_rope* r); /* NULL is a no-op */
+
+/*
+ * tq_qk_norm_rope -- what a query and a key go through between a model's
+ * projection and this library's encoders and attention, in one pass over
+ * both: per head an RMS norm, x / sqrt(mean(x^2) + eps) * w, then the
+ * rotation of `rope`.  Sums and rotation in fp32, one rounding at the end.
+ * The angle pos * f is reduced to a fraction of a turn exactly (64-bit fixed
+ * point), so far positions lose nothing.
+ *   rope    NULL: no rotation
+ *   x       q and k each: DEVICE, n_tok x H heads of d elements of dtype dt,
+ *           element strides q_tok / q_head (k_tok / k_head) between tokens and
+ *           heads, d contiguous; the heads of one fused projection can be
+ *           given in place.  H may be 0 (the pointer is then not read).
+ *   pos     DEVICE int64[n_tok] (read only with rope; any value)
+ *   wq, wk  DEVICE d weights of dtype dt each; NULL: that side has no norm
+ *   eps     >= 0
+ *   q_out, k_out  outputs of dtype dt with strides of their own.  May be the
+ *           inputs (same pointer and strides), must not overlap them otherwise.
+ *   d       1..4096, >= rot
+ * Any element alignment and any strides >= 0 of the inputs; the outputs'
+ * rows must not overlap one another.
+ */
+tq_status tq_qk_norm_rope(const tq_rope* rope, tq_dtype dt, int64_t n_tok, int d, int Hq,
+                          const void* q, int64_t q_tok, int64_t q_head, int Hkv, const void* k,
+                          int64_t k_tok, int64_t k_head, const int64_t* pos, const void* wq,
+                          const void* wk, float eps, void* q_out, int64_t qo_tok, int64_t qo_head,
+                          void* k_out, int64_t ko_tok, int64_t ko_head, void* stream);
+
+/*
+ * tq_paged_create -- describe a paged compressed KV cache: Q_prod keys and
+ * Q_MSE values of `layers` layers and Hkv KV heads in pages of `page` tokens
+ * (a multiple of 32).
+ *   kp, vp  as tq_decode_attention (same d; Hadamard rotation, else
+ *           TQ_ERR_UNSUPPORTED); both must outlive the handle
+ *   layers 1..4096, Hkv 1..1024, page 32..65536
+ *
+ * The pool is one caller-owned DEVICE array uint32 [n_pages][page_words],
+ * 16-byte aligned, n_pages < 2^31; a page is [layers][Hkv][page / 32] block
+ * records of block_words words each (tq_paged_info).  A record holds
+ * everything of 32 consecutive tokens of one layer and KV head, so one copy
+ * brings it in:
+ *   key words    nk = code words + sign words of a token (ROW order, the signs
+ *                behind the codes), in granules of g = 4, 2 or 1 words (the
+ *                largest that divides nk): uint32 [nk / g][32][g]
+ *   key norms    float [32]
+ *   residual norms  float [32], or uint16 [32] with TQ_STORE_RNORM_F16
+ *   value words  uint32 [k][d_pad], the k bits of token t at, with s = t mod 4
+ *                and i = t div 4:
+ *                  k = 1     bit t of word 0
+ *                  k = 2, 3  index bits 0..1 at bits 4 i + 2 (s mod 2) of word
+ *                            s div 2; for k = 3 index bit 2 at bit (t + 2) mod
+ *                            32 of word 2
+ *                  k = 4     bits 4 i .. 4 i + 3 of word s: 0..7 for index 8 +
+ *                            x, 8 + x for index 7 - x
+ *   value norms  float [32]
+ *
+ * A page table is DEVICE int32 [B][table_ld >= max_pages]: entry i of row b is
+ * the page of tokens [i page, (i + 1) page) of sequence b.  A page may stand
+ * in several rows (a shared prefix).  An entry outside [0, n_pages) is a hole:
+ * nothing is read or written there and its tokens take no part.  Lengths are
+ * DEVICE int32 [B], read as 0 where negative and as max_pages * page where
+ * longer.  max_pages * page must be below 2^31.
+ *
+ * The lengths and tables are read on the device only: a captured graph can be
+ * replayed as sequences grow, fork and end.
+ */
+typedef struct tq_paged tq_paged; /* opaque cache description */
+tq_status tq_paged_create(const tq_params* kp, const tq_params* vp, int layers, int Hkv, int page,
+                          tq_paged** out);
+tq_status tq_paged_destroy(tq_paged* pg); /* NULL is a no-op */
+/* words of a block record and of a page (any pointer may be NULL) */
+tq_status tq_paged_info(const tq_paged* pg, int* block_words, int64_t* page_words);
+
+/*
+ * tq_paged_append -- write encoded tokens into the pages of one layer.  The
+ * rows are the encoders' ROW outputs for vectors [n_tok][Hkv] (kcodes, ksigns,
+ * knorms, krnorms of tq_encode_prod; vcodes, vnorms of tq_encode_mse), the new
+ * tokens of sequence b being rows cu[b] .. cu[b + 1] - 1, written to
+ * positions start[b], start[b] + 1, ...
+ *   cu      DEVICE int32 [B + 1], ascending, 0 <= cu[0], cu[B] <= n_tok; rows
+ *           outside [cu[0], cu[B]) are ignored.  NULL: one token per sequence
+ *           (n_tok = B)
+ *   start   DEVICE int32 [B]; tokens at negative positions, at positions
+ *           beyond max_pages * page and in holes are dropped
+ * Only the new tokens' slots change; the other tokens of a block are kept.
+ * Two sequences must not append to the same page in one call.  The lengths
+ * are the caller's to advance.
+ */
+tq_status tq_paged_append(const tq_paged* pg, uint32_t* pool, int64_t n_pages, int layer,
+                          const uint32_t* kcodes, const uint32_t* ksigns, const float* knorms,
+                          const float* krnorms, const uint32_t* vcodes, const float* vnorms,
+                          int64_t n_tok, int B, const int32_t* cu, const int32_t* start,
+                          const int32_t* tables, int64_t table_ld, int max_pages, void* stream);
+
+/*
+ * tq_paged_attention -- tq_decode_attention over a paged cache: one query
+ * token per sequence against the first lens[b] tokens of its pages, the work
+ * split evenly over the GPU whatever the lengths, the parts joined by their
+ * log-sum-exp in a fixed order.
+ *   q       DEVICE [B][Hq][d] of dtype dt, q_ld >= Hq d elements between
+ *           sequences, 16-byte aligned rows not required; at most 16 query
+ *           heads per KV head, and at most 51200 entries of q' and u per KV head,
+ *           (Hq / Hkv) (d_pad + m) (TQ_ERR_UNSUPPORTED above)
+ *   out     DEVICE [B][Hq][d] of dtype dt (rounded once); rows of sequences
+ *           with no token are 0
+ *   lse     DEVICE float [B][Hq] or NULL: log(sum(exp(scale * s))), -inf
+ *           where there is no token; joins the result with attention over
+ *           tokens that are not in the cache
+ *   ws      tq_paged_attention_workspace_size bytes, 256-byte aligned,
+ *           nothing kept in it between calls: calls that overlap on the GPU
+ *           need one each
+ */
+tq_status tq_paged_attention(const tq_paged* pg, const void* q, tq_dtype dt, int64_t q_ld, int B,
+                             int Hq, const uint32_t* pool, int64_t n_pages, int layer,
+                             const int32_t* lens, const int32_t* tables, int64_t table_ld,
+                             int max_pages, float scale, void* out, float* lse, void* ws,
+                             size_t ws_bytes, void* stream);
+tq_status tq_paged_attention_workspace_size(const tq_paged* pg, int B, int Hq, size_t* bytes);
+
+/*
+ * tq_paged_fork -- sequences that begin as copies of others: for each i <
+ * n, row children[i] of the table becomes row parents[i] (its pages shared,
+ * -1 behind them) and lens[children[i]] = lens[parents[i]]; where the
+ * parent's last page is partly filled, the child gets page fresh[i] in its
+ * place, and the blocks of it that hold tokens are copied for every layer and
+ * head.  fresh[i] is not read into the table where the last page is full.
+ *   parents, children, fresh  DEVICE int32 [n]; an i whose parent or child is
+ *           outside [0, B) is skipped; where the fresh page is outside [0,
+ *           n_pages) or the parent's last page is a hole, the child has a hole
+ *           there and nothing is copied
+ * The children must differ from one another and from every parent, and the
+ * fresh pages (where used) from one another and from the parents' pages.
+ */
+tq_status tq_paged_fork(const tq_paged* pg, uint32_t* pool, int64_t n_pages, int32_t* tables,
+                        int64_t table_ld, int max_pages, int32_t* lens, int B,
+                        const int32_t* parents, const int32_t* children, const int32_t* fresh,
+                        int n, void* stream);
+
+/*
+ * tq_paged_compact -- free what no sequence needs and move the rest
+ * together: the pages that the first ceil(lens[b] / page) entries of some row
+ * name are in use, *n_used in number; those at n_used and behind are moved
+ * (in ascending order) to the unused ones below n_used (in ascending order),
+ * and tables_out names the pages' new places, -1 in holes and behind a row's
+ * last used entry.  Afterwards pages n_used .. n_pages - 1 are free.  A
+ * sequence ends by setting its length to 0.
+ *   tables_out  DEVICE int32 [B][table_ld]; may be `tables`
+ *   n_used      DEVICE int32 [1]
+ *   ws          tq_paged_compact_workspace_size bytes, 256-byte aligned
+ */
+tq_status tq_paged_compact(const tq_paged* pg, uint32_t* pool, int64_t n_pages,
+                           const int32_t* tables, int32_t* tables_out, int64_t table_ld,
+                           int max_pages, const int32_t* lens, int B, int32_t* n_used, void* ws,
+                           size_t ws_bytes, void* stream);
+tq_status tq_paged_compact_workspace_size(int64_t n_pages, size_t* bytes);
+
+/*
  * tq_sync_check -- synchronize `stream` and report (then clear) the device
  * error word that kernels set when a bounded wait expires (TQ_ERR_TIMEOUT)
  * or an internal check fails (TQ_ERR_INTERNAL).  When it reports

@@ -15,15 +15,17 @@ import numpy as np
 
 from . import _lib as L
 from ._lib import (BF16, F16, F32, LAYOUT_BLOCK32, LAYOUT_ROW, MODE_MSE, MODE_MSE_UNBIASED, MODE_PROD,  # noqa: F401
-                   ROT_DENSE, ROT_HADAMARD, STORE_RNORM_F16, TQError)
+                   ROPE_BANDS, ROPE_LINEAR, ROPE_PLAIN, ROPE_YARN, ROT_DENSE, ROT_HADAMARD, STORE_RNORM_F16, TQError)
 
 __all__ = [
     "TQParams", "tq_build_codebook", "tq_make_rotation", "tq_params_create", "tq_encode_mse", "tq_encode_prod",
     "tq_decode", "tq_scores", "tq_decode_attention", "tq_decode_attention_workspace_size",
     "tq_decode_attention_noalloc", "tq_decode_step", "tq_decode_step_workspace_size",
+    "TQRope", "tq_qk_norm_rope", "TQPaged", "tq_paged_append", "tq_paged_attention",
+    "tq_paged_attention_workspace_size", "tq_paged_fork", "tq_paged_compact", "tq_paged_compact_workspace_size",
     "tq_check_wait_expiry", "tq_sync_check", "tq_version", "lib_path", "TQError",
     "F32", "F16", "BF16", "LAYOUT_ROW", "LAYOUT_BLOCK32", "MODE_MSE", "MODE_PROD", "MODE_MSE_UNBIASED",
-    "STORE_RNORM_F16", "ROT_HADAMARD", "ROT_DENSE",
+    "STORE_RNORM_F16", "ROT_HADAMARD", "ROT_DENSE", "ROPE_PLAIN", "ROPE_LINEAR", "ROPE_BANDS", "ROPE_YARN",
 ]
 
 
@@ -319,6 +321,251 @@ def tq_decode_step(kp: TQParams, vp: TQParams, q, k_new, v_new, kcache, vcache, 
         float(scale), _ptr(kcodes), _ptr(ksigns), _ptr(knorms), _ptr(krnorms), _ptr(vcodes),
         _ptr(vnorms), _ptr(out), _ptr(ws), ws.numel(), _stream(stream)))
     return out
+
+
+class TQRope:
+    """Handle of one rotary position embedding (tq_rope_create)."""
+
+    def __init__(self, rot: int, base: float = 10000.0, interleaved: bool = False, scaling: int = ROPE_PLAIN,
+                 factor: float = 1.0, orig_len: float = 0.0, low: float = 0.0, high: float = 0.0):
+        self._h = C.c_void_p()
+        L.check("tq_rope_create", L.lib().tq_rope_create(
+            rot, int(interleaved), base, scaling, factor, orig_len, low, high, C.byref(self._h)))
+        self.rot, self.interleaved = rot, bool(interleaved)
+
+    @property
+    def handle(self):
+        return self._h
+
+    def close(self):
+        if self._h:
+            L.lib().tq_rope_destroy(self._h)
+            self._h = C.c_void_p()
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def _on(device, *tensors):
+    """The device that every given tensor is on, and an int32/int64/float check left to the callers."""
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"a tensor on {t.device} beside one on {device}")
+    if device.type != "cuda":
+        raise ValueError(f"tensors on {device}: a CUDA device is needed")
+    return _torch().cuda.device(device)
+
+
+def _int32(name, t, shape):
+    torch = _torch()
+    if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous int32 {tuple(shape)}")
+
+
+def _heads(name, x, n, d, dtype):
+    """Token and head strides of a [n, heads, d] tensor whose last dimension is contiguous."""
+    if x.dim() != 3 or x.shape[0] != n or x.shape[2] != d or x.dtype != dtype:
+        raise ValueError(f"{name} must be [{n}, heads, {d}] {dtype}")
+    if x.numel() and d > 1 and x.stride(2) != 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    return x.stride(0), x.stride(1)
+
+
+def tq_qk_norm_rope(rope: Optional[TQRope], q, k, pos=None, wq=None, wk=None, eps: float = 1e-6,
+                    q_out=None, k_out=None, stream=None):
+    """RMS norm per head (weights wq, wk [d]; None: no norm) and rotary
+    positions (pos int64 [n]; rope None: no rotation) of q [n, Hq, d] and k
+    [n, Hkv, d] (k may be None), any token and head strides.  Returns (q_out,
+    k_out); the outputs may be the inputs."""
+    torch = _torch()
+    n, Hq, d = q.shape
+    qs = _heads("q", q, n, d, q.dtype)
+    if q_out is None:
+        q_out = torch.empty((n, Hq, d), dtype=q.dtype, device=q.device)
+    qos = _heads("q_out", q_out, n, d, q.dtype)
+    Hkv, ks, kos = 0, (0, 0), (0, 0)
+    if k is not None:
+        ks, Hkv = _heads("k", k, n, d, q.dtype), k.shape[1]
+        if k_out is None:
+            k_out = torch.empty((n, Hkv, d), dtype=q.dtype, device=q.device)
+        kos = _heads("k_out", k_out, n, d, q.dtype)
+        if k_out.shape != k.shape:
+            raise ValueError("k_out must have the shape of k")
+    if q_out.shape != q.shape:
+        raise ValueError("q_out must have the shape of q")
+    if rope is not None and (pos is None or pos.dtype != torch.int64 or tuple(pos.shape) != (n,) or
+                             not pos.is_contiguous()):
+        raise ValueError(f"pos must be contiguous int64 [{n}]")
+    for name, w in (("wq", wq), ("wk", wk)):
+        if w is not None and (w.dtype != q.dtype or tuple(w.shape) != (d,) or not w.is_contiguous()):
+            raise ValueError(f"{name} must be contiguous [{d}] {q.dtype}")
+    with _on(q.device, k, pos, wq, wk, q_out, k_out):
+        L.check("tq_qk_norm_rope", L.lib().tq_qk_norm_rope(
+            None if rope is None else rope.handle, _dtype_code(q), n, d, Hq, _ptr(q), *qs, Hkv, _ptr(k), *ks,
+            _ptr(pos), _ptr(wq), _ptr(wk), eps, _ptr(q_out), *qos, _ptr(k_out), *kos, _stream(stream)))
+    return q_out, k_out
+
+
+class TQPaged:
+    """Handle of one paged compressed cache (tq_paged_create); keeps its quantizers."""
+
+    def __init__(self, kp: TQParams, vp: TQParams, layers: int, hkv: int, page: int):
+        self._h = C.c_void_p()
+        L.check("tq_paged_create", L.lib().tq_paged_create(kp.handle, vp.handle, layers, hkv, page, C.byref(self._h)))
+        bw, pw = C.c_int(), C.c_int64()
+        L.check("tq_paged_info", L.lib().tq_paged_info(self._h, C.byref(bw), C.byref(pw)))
+        self.kp, self.vp, self.layers, self.hkv, self.page = kp, vp, layers, hkv, page
+        self.block_words, self.page_words = bw.value, pw.value
+
+    @property
+    def handle(self):
+        return self._h
+
+    def new_pool(self, n_pages: int, device="cuda"):
+        """An int32 [n_pages, page_words] pool of zeros."""
+        torch = _torch()
+        return torch.zeros((n_pages, self.page_words), dtype=torch.int32, device=device)
+
+    def close(self):
+        if self._h:
+            L.lib().tq_paged_destroy(self._h)
+            self._h = C.c_void_p()
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def _pool(pg, pool):
+    torch = _torch()
+    if pool.dtype != torch.int32 or pool.dim() != 2 or pool.shape[1] != pg.page_words or not pool.is_contiguous():
+        raise ValueError(f"pool must be contiguous int32 [n_pages, {pg.page_words}]")
+    return _ptr(pool), pool.shape[0]
+
+
+def _table(name, t, B):
+    torch = _torch()
+    if t.dtype != torch.int32 or t.dim() != 2 or t.shape[0] != B or (t.numel() and t.stride(1) != 1):
+        raise ValueError(f"{name} must be int32 [{B}, max_pages] with contiguous rows")
+    return _ptr(t), max(t.stride(0), t.shape[1]) if B > 1 else t.shape[1], t.shape[1]
+
+
+def tq_paged_append(pg: TQPaged, pool, layer: int, keys, values, start, tables, cu=None, stream=None):
+    """Write encoded tokens into the pages of a layer.  keys = (codes, signs,
+    norms, rnorms) of tq_encode_prod and values = (codes, norms) of
+    tq_encode_mse (ROW layout) for rows [n_tok, Hkv]; the tokens cu[b] ..
+    cu[b + 1] - 1 (cu int32 [B + 1]; None: token b) go to the positions from
+    start[b] (int32 [B]) on of sequence b, whose pages are tables[b]."""
+    torch = _torch()
+    B = start.shape[0]
+    kcodes, ksigns, knorms, krnorms = keys
+    vcodes, vnorms = values
+    rows = knorms.numel()
+    n_tok = rows // pg.hkv
+    if rows != n_tok * pg.hkv:
+        raise ValueError(f"{rows} rows are no multiple of {pg.hkv} heads")
+    words = (("key codes", kcodes, pg.kp.code_words, torch.int32), ("signs", ksigns, pg.kp.sign_words, torch.int32),
+             ("key norms", knorms, 1, torch.float32), ("residual norms", krnorms, 1, getattr(torch, pg.kp.rnorm_dtype)),
+             ("value codes", vcodes, pg.vp.code_words, torch.int32), ("value norms", vnorms, 1, torch.float32))
+    for name, t, w, dt in words:
+        if t.dtype != dt or t.numel() != rows * w or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous {dt} with {w} words for each of {rows} rows")
+    _int32("start", start, (B,))
+    if cu is not None:
+        _int32("cu", cu, (B + 1,))
+    elif n_tok != B:
+        raise ValueError(f"{n_tok} tokens for {B} sequences need cu")
+    with _on(pool.device, kcodes, ksigns, knorms, krnorms, vcodes, vnorms, start, tables, cu):
+        L.check("tq_paged_append", L.lib().tq_paged_append(
+            pg.handle, *_pool(pg, pool), layer, _ptr(kcodes), _ptr(ksigns), _ptr(knorms), _ptr(krnorms),
+            _ptr(vcodes), _ptr(vnorms), n_tok, B, _ptr(cu), _ptr(start), *_table("tables", tables, B), _stream(stream)))
+
+
+def tq_paged_attention_workspace_size(pg: TQPaged, B: int, Hq: int) -> int:
+    need = C.c_size_t()
+    L.check("tq_paged_attention_workspace_size", L.lib().tq_paged_attention_workspace_size(
+        pg.handle, B, Hq, C.byref(need)))
+    return need.value
+
+
+def tq_paged_attention(pg: TQPaged, q, pool, layer: int, lens, tables, scale: float, out=None, lse=None,
+                       want_lse: bool = False, ws=None, stream=None):
+    """One query token per sequence: q [B, Hq, d] (fp32, fp16 or bf16; any
+    stride between sequences) over the first lens[b] (int32 [B]) tokens of the
+    pages tables[b].  Returns out [B, Hq, d] of q's dtype, or (out, lse [B, Hq]
+    fp32) with want_lse."""
+    torch = _torch()
+    B, Hq, d = q.shape
+    if d != pg.kp.d:
+        raise ValueError(f"last dimension {d} != d {pg.kp.d}")
+    if q.numel() and (q.stride(2) != 1 or q.stride(1) != d or (B > 1 and q.stride(0) < Hq * d)):
+        q = q.contiguous()
+    _int32("lens", lens, (B,))
+    if out is None:
+        out = torch.empty((B, Hq, d), dtype=q.dtype, device=q.device)
+    if out.dtype != q.dtype or tuple(out.shape) != (B, Hq, d) or not out.is_contiguous():
+        raise ValueError(f"out must be contiguous [{B}, {Hq}, {d}] {q.dtype}")
+    if lse is None and want_lse:
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (B, Hq) or not lse.is_contiguous()):
+        raise ValueError(f"lse must be contiguous float32 [{B}, {Hq}]")
+    with _on(q.device, pool, lens, tables, out, lse, ws):
+        if ws is None:
+            ws = _ws(tq_paged_attention_workspace_size(pg, B, Hq), q.device)
+        L.check("tq_paged_attention", L.lib().tq_paged_attention(
+            pg.handle, _ptr(q), _dtype_code(q), max(q.stride(0), Hq * d), B, Hq, *_pool(pg, pool), layer, _ptr(lens),
+            *_table("tables", tables, B), float(scale), _ptr(out), _ptr(lse), _ptr(ws),
+            0 if ws is None else ws.numel(), _stream(stream)))
+    return (out, lse) if want_lse else out
+
+
+def tq_paged_fork(pg: TQPaged, pool, tables, lens, parents, children, fresh, stream=None):
+    """Make sequences children[i] copies of parents[i]: table rows, lengths and
+    (into page fresh[i]) the partly filled last page.  All int32; tables and
+    lens are updated in place."""
+    B, n = lens.shape[0], parents.shape[0]
+    _int32("lens", lens, (B,))
+    for name, t in (("parents", parents), ("children", children), ("fresh", fresh)):
+        _int32(name, t, (n,))
+    with _on(pool.device, tables, lens, parents, children, fresh):
+        L.check("tq_paged_fork", L.lib().tq_paged_fork(
+            pg.handle, *_pool(pg, pool), *_table("tables", tables, B), _ptr(lens), B, _ptr(parents), _ptr(children),
+            _ptr(fresh), n, _stream(stream)))
+
+
+def tq_paged_compact_workspace_size(n_pages: int) -> int:
+    need = C.c_size_t()
+    L.check("tq_paged_compact_workspace_size", L.lib().tq_paged_compact_workspace_size(n_pages, C.byref(need)))
+    return need.value
+
+
+def tq_paged_compact(pg: TQPaged, pool, tables, lens, tables_out=None, n_used=None, ws=None, stream=None):
+    """Move the pages that the sequences use to the lowest numbers and rewrite
+    the tables (into tables_out; None: in place).  Returns n_used (int32 [1], on
+    the device): pages n_used and behind are free."""
+    torch = _torch()
+    B = lens.shape[0]
+    _int32("lens", lens, (B,))
+    if tables_out is None:
+        tables_out = tables
+    if n_used is None:
+        n_used = torch.empty(1, dtype=torch.int32, device=pool.device)
+    _int32("n_used", n_used, (1,))
+    if tables_out.shape != tables.shape or tables_out.stride() != tables.stride():
+        raise ValueError("tables_out must have the shape and strides of tables")
+    tab = _table("tables", tables, B)
+    with _on(pool.device, tables, tables_out, lens, n_used, ws):
+        if ws is None:
+            ws = _ws(tq_paged_compact_workspace_size(pool.shape[0]), pool.device)
+        L.check("tq_paged_compact", L.lib().tq_paged_compact(
+            pg.handle, *_pool(pg, pool), tab[0], _table("tables_out", tables_out, B)[0], *tab[1:], _ptr(lens), B,
+            _ptr(n_used), _ptr(ws), ws.numel(), _stream(stream)))
+    return n_used
 
 
 def tq_check_wait_expiry(budget_cycles: int, stream=None):

@@ -19,6 +19,7 @@ ROT_HADAMARD, ROT_DENSE = 0, 1
 MODE_MSE, MODE_PROD, MODE_MSE_UNBIASED = 0, 1, 2
 STORE_RNORM_F16 = 0x100  # OR'ed into MODE_PROD: residual norms stored as fp16
 LAYOUT_ROW, LAYOUT_BLOCK32 = 0, 1
+ROPE_PLAIN, ROPE_LINEAR, ROPE_BANDS, ROPE_YARN = 0, 1, 2, 3
 
 # exported symbol -> (restype, argtypes)
 _vp, _i, _i64, _f, _sz = C.c_void_p, C.c_int, C.c_int64, C.c_float, C.c_size_t
@@ -46,6 +47,21 @@ SIGNATURES = {
     "tq_decode_step_workspace_size": (_i, [_vp, _vp, _i, _i, _i, _i, _i64, C.POINTER(_sz)]),
     "tq_decode_step": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i64, _i64, _f,
                             _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "tq_rope_create": (_i, [_i, _i, C.c_double, _i, C.c_double, C.c_double, C.c_double, C.c_double, C.POINTER(_vp)]),
+    "tq_rope_destroy": (_i, [_vp]),
+    "tq_qk_norm_rope": (_i, [_vp, _i, _i64, _i, _i, _vp, _i64, _i64, _i, _vp, _i64, _i64, _vp, _vp, _vp, _f,
+                             _vp, _i64, _i64, _vp, _i64, _i64, _vp]),
+    "tq_paged_create": (_i, [_vp, _vp, _i, _i, _i, C.POINTER(_vp)]),
+    "tq_paged_destroy": (_i, [_vp]),
+    "tq_paged_info": (_i, [_vp, C.POINTER(_i), C.POINTER(_i64)]),
+    "tq_paged_append": (_i, [_vp, _vp, _i64, _i, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i, _vp, _vp,
+                             _vp, _i64, _i, _vp]),
+    "tq_paged_attention_workspace_size": (_i, [_vp, _i, _i, C.POINTER(_sz)]),
+    "tq_paged_attention": (_i, [_vp, _vp, _i, _i64, _i, _i, _vp, _i64, _i, _vp, _vp, _i64, _i, _f,
+                                _vp, _vp, _vp, _sz, _vp]),
+    "tq_paged_fork": (_i, [_vp, _vp, _i64, _vp, _i64, _i, _vp, _i, _vp, _vp, _vp, _i, _vp]),
+    "tq_paged_compact_workspace_size": (_i, [_i64, C.POINTER(_sz)]),
+    "tq_paged_compact": (_i, [_vp, _vp, _i64, _vp, _vp, _i64, _i, _vp, _i, _vp, _vp, _sz, _vp]),
     "tq_sync_check": (_i, [_vp]),
     "tq_check_wait_expiry": (_i, [C.c_int64, _vp]),
 }

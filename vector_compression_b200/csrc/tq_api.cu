@@ -441,6 +441,9 @@ int launch_topk(const float* scores, int64_t nq, int64_t n_vec, int topk, float*
   return cudaGetLastError();
 }
 
+int sm_count() { return num_sms(); }
+unsigned* error_word() { return device_error_ptr(); }
+
 size_t attention_workspace(const QParams& kp, const QParams& vp, int L, int B, int Hq, int Hkv,
                            int64_t seq, int* chunk_out, int* n_chunks_out) {
   const int64_t groups = (int64_t)L * B * Hkv;

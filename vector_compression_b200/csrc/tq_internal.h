@@ -80,5 +80,7 @@ int launch_decode_attention(const QParams& kp, const QParams& vp, const float* q
                             const float* krnorms, const uint32_t* vcodes, const float* vnorms,
                             float* out, void* ws, void* stream);
 int read_and_clear_device_error(void* stream, unsigned* err);
+int sm_count();          // SMs of the current device
+unsigned* error_word();  // the device error word of the current context, null when it cannot be had
 
 }  // namespace tq

@@ -1,0 +1,467 @@
+// The paged compressed cache: its description, the append of encoded tokens,
+// and the page operations fork and compaction (include/tq.h).  All of them move
+// bits and nothing else; memory traffic and launch latency are what they cost.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <new>
+
+#include "tq_device.cuh"
+#include "tq_paged.h"
+
+namespace tq {
+namespace paged {
+namespace {
+
+inline bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool al256(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
+
+// ---------------------------------------------------------------- append
+
+struct AppendArgs {
+  Layout L;
+  Table tab;
+  uint32_t* pool;
+  int layer;
+  const uint32_t *kcodes, *ksigns, *vcodes;
+  const float *knorms, *krnorms, *vnorms;
+  int64_t n_tok;
+  int B;
+  const int32_t *cu, *start;
+};
+
+// Transposes a 32 x 32 bit matrix held one row per lane: afterwards bit t of
+// lane j's word is bit j of lane t's.
+__device__ __forceinline__ uint32_t transpose32(uint32_t w, int lane) {
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) {
+    // the lanes with bit s swap their low parts with the partners' high parts
+    const uint32_t m = s == 16 ? 0x0000ffffu : s == 8 ? 0x00ff00ffu : s == 4 ? 0x0f0f0f0fu : s == 2 ? 0x33333333u : 0x55555555u;
+    const uint32_t o = __shfl_xor_sync(0xffffffffu, w, s);
+    w = (lane & s) ? ((w & ~m) | ((o >> s) & m)) : ((w & m) | ((o << s) & ~m));
+  }
+  return w;
+}
+
+// The first and last+1 new token (packed numbers) of the sequence that token i
+// belongs to, and its number; false when i belongs to none.
+__device__ __forceinline__ bool find_sequence(const AppendArgs& A, int64_t i, int& b, int64_t& t0, int64_t& t1) {
+  if (!A.cu) {
+    b = (int)i;
+    t0 = i;
+    t1 = i + 1;
+    return true;
+  }
+  if (i < A.cu[0] || i >= A.cu[A.B]) return false;
+  int lo = 0, hi = A.B;  // cu[lo] <= i < cu[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (A.cu[mid] <= i) lo = mid;
+    else hi = mid;
+  }
+  b = lo;
+  t0 = A.cu[lo];
+  t1 = A.cu[hi];
+  return t0 <= i && t1 <= A.n_tok;
+}
+
+// A warp writes the new tokens that one 32-token block of one head gets (a run).
+// It is started for every token and goes on only for a run's first one.
+__global__ void __launch_bounds__(128) append_kernel(const AppendArgs A) {
+  const Layout& L = A.L;
+  const int lane = threadIdx.x & 31;
+  const int64_t item = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  const int64_t tok = item / L.hkv;
+  const int h = (int)(item - tok * L.hkv);
+  if (tok >= A.n_tok) return;
+  int b;
+  int64_t t0, t1;
+  if (!find_sequence(A, tok, b, t0, t1)) return;
+  const int64_t pos = A.start[b] + (tok - t0);
+  if (pos < 0 || pos >= (int64_t)A.tab.max_pages * L.page) return;
+  const int off = (int)(pos & 31);
+  // the first token at position 0 of a sequence that starts before it begins a run too: 0 mod 32
+  if (tok != t0 && off != 0) return;
+  const int len = (int)min64(32 - off, t1 - tok);
+  const int64_t at = record_at(L, A.tab, b, (int)(pos >> 5), A.layer, h);
+  if (at < 0) return;
+  uint32_t* rec = A.pool + at;
+  const int64_t row0 = tok * L.hkv + h;  // row of token tok + i: row0 + i hkv
+  for (int e = lane; e < len * L.nk; e += 32) {
+    const int i = e / L.nk, w = e - i * L.nk;
+    const int64_t row = row0 + (int64_t)i * L.hkv;
+    rec[key_word_at(L, off + i, w)] = w < L.kw ? A.kcodes[row * L.kw + w] : A.ksigns[row * L.sw + (w - L.kw)];
+  }
+  const bool mine = lane >= off && lane < off + len;  // lane: place in the block
+  const int64_t row = row0 + (int64_t)(lane - off) * L.hkv;
+  if (mine) {
+    rec[L.o_kn + lane] = __float_as_uint(A.knorms[row]);
+    rec[L.o_vn + lane] = __float_as_uint(A.vnorms[row]);
+    if (L.r16)
+      reinterpret_cast<uint16_t*>(rec + L.o_kr)[lane] = reinterpret_cast<const uint16_t*>(A.krnorms)[row];
+    else
+      rec[L.o_kr + lane] = __float_as_uint(A.krnorms[row]);
+  }
+  const uint32_t own = (len == 32 ? 0xffffffffu : ((1u << len) - 1u)) << off;  // the run's tokens
+  const int wpp = L.dp / 32;
+  // bits of the plane words p (bit t: token t) that go to value word q
+  auto place = [&](const uint32_t (&p)[4], int q) -> uint32_t {
+    if (L.kv == 1) return p[0];
+    if (L.kv == 4) {
+      // sign and magnitude: bit 3 below zero, bits 0..2 the distance from the middle
+      const uint32_t n = ~p[3];
+      const uint32_t m = 0x11111111u;
+      return (((p[0] ^ n) >> q) & m) | ((((p[1] ^ n) >> q) & m) << 1) | ((((p[2] ^ n) >> q) & m) << 2) |
+             (((n >> q) & m) << 3);
+    }
+    if (q == 2) return __funnelshift_l(p[2], p[2], 2);
+    const uint32_t m = 0x11111111u;
+    const int s = 2 * q;
+    return ((p[0] >> s) & m) | (((p[1] >> s) & m) << 1) | (((p[0] >> (s + 1)) & m) << 2) | (((p[1] >> (s + 1)) & m) << 3);
+  };
+  for (int jw = 0; jw < wpp; ++jw) {
+    uint32_t p[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (q < L.kv) p[q] = transpose32(mine ? A.vcodes[row * (L.kv * wpp) + q * wpp + jw] : 0u, lane);
+    for (int q = 0; q < L.kv; ++q) {
+      uint32_t* w = rec + L.o_v + q * L.dp + 32 * jw + lane;
+      // the mask of the run's fields: the same placement of a code of ones
+      // (for k = 4 of the fields' four bits)
+      uint32_t f[4] = {own, own, own, own};
+      uint32_t msk;
+      if (L.kv == 4) {
+        const uint32_t m = (own >> q) & 0x11111111u;
+        msk = m * 15u;
+      } else {
+        msk = place(f, q);
+      }
+      const uint32_t v = place(p, q) & msk;
+      *w = own == 0xffffffffu ? v : ((*w & ~msk) | v);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- copying
+
+// Copies n 16-byte words by the calling warp, four in flight per lane.
+__device__ __forceinline__ void warp_copy(uint4* dst, const uint4* src, int64_t n, int lane) {
+  int64_t i = lane;
+  for (; i + 96 < n; i += 128) {
+    const uint4 a = src[i], b = src[i + 32], c = src[i + 64], d = src[i + 96];
+    dst[i] = a;
+    dst[i + 32] = b;
+    dst[i + 64] = c;
+    dst[i + 96] = d;
+  }
+  for (; i < n; i += 32) dst[i] = src[i];
+}
+
+struct ForkArgs {
+  Layout L;
+  uint32_t* pool;
+  int64_t n_pages;
+  int32_t* tables;
+  int64_t ld;
+  int max_pages;
+  int32_t* lens;
+  int B;
+  const int32_t *parents, *children, *fresh;
+  int n;
+};
+
+// Item (i, segment): a warp copies the used blocks of the tail page of fork i
+// for one layer and head; segment 0's warp also writes the child's table row
+// and length.
+__global__ void __launch_bounds__(256) fork_kernel(const ForkArgs A) {
+  const Layout& L = A.L;
+  const int lane = threadIdx.x & 31;
+  const int64_t segs = (int64_t)L.layers * L.hkv;
+  const int64_t warps = ((int64_t)gridDim.x * blockDim.x) >> 5;
+  for (int64_t item = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; item < A.n * segs; item += warps) {
+    const int i = (int)(item / segs);
+    const int64_t seg = item - i * segs;
+    const int par = A.parents[i], ch = A.children[i];
+    if (par < 0 || par >= A.B || ch < 0 || ch >= A.B) continue;
+    const int len = clamp_len(A.lens[par], L, A.max_pages);
+    const int full = len / L.page, rest = len - full * L.page;
+    const int32_t* from = A.tables + par * A.ld;
+    const int fresh = A.fresh[i];
+    // a hole stays one: there is nothing to copy into a fresh page
+    const int32_t src = rest ? from[full] : -1;
+    const bool ok = src >= 0 && src < A.n_pages && fresh >= 0 && fresh < A.n_pages;
+    if (seg == 0) {
+      int32_t* to = A.tables + ch * A.ld;
+      for (int p = lane; p < A.max_pages; p += 32)
+        to[p] = p < full ? from[p] : (p == full && ok) ? fresh : -1;
+      if (lane == 0) A.lens[ch] = len;
+    }
+    if (!ok) continue;
+    const int64_t at = seg * L.nb * L.words;
+    warp_copy(reinterpret_cast<uint4*>(A.pool + fresh * L.page_words + at),
+              reinterpret_cast<const uint4*>(A.pool + src * L.page_words + at),
+              (int64_t)((rest + 31) / 32) * (L.words / 4), lane);
+  }
+}
+
+// ---------------------------------------------------------------- compaction
+
+struct CompactArgs {
+  Layout L;
+  uint32_t* pool;
+  int64_t n_pages;
+  const int32_t* tables;
+  int32_t* tables_out;
+  int64_t ld;
+  int max_pages;
+  const int32_t* lens;
+  int B;
+  int32_t* n_used;
+  // workspace
+  uint32_t* used;   // a bit per page
+  int32_t* rank;    // per page: number among the pages to move, -1 for the others
+  int32_t* from;    // pages to move, ascending
+  int32_t* to;      // unused pages below n_used, ascending
+  int32_t* moves;   // how many
+};
+
+// The page that entry p of row b names, -1 where the row does not need one.
+__device__ __forceinline__ int32_t live_entry(const CompactArgs& A, int64_t b, int p) {
+  const int len = clamp_len(A.lens[b], A.L, A.max_pages);
+  if ((int64_t)p * A.L.page >= len) return -1;
+  const int32_t id = A.tables[b * A.ld + p];
+  return id < 0 || id >= A.n_pages ? -1 : id;
+}
+
+__global__ void __launch_bounds__(256) mark_kernel(const CompactArgs A) {
+  const int64_t n = (int64_t)A.B * A.max_pages;
+  for (int64_t e = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; e < n; e += (int64_t)gridDim.x * blockDim.x) {
+    const int64_t b = e / A.max_pages;
+    const int32_t id = live_entry(A, b, (int)(e - b * A.max_pages));
+    if (id >= 0) atomicOr(&A.used[id >> 5], 1u << (id & 31));  // bits: the order does not matter
+  }
+}
+
+// Each block owns 256 words of the bit map; it counts the words before its own
+// and all words itself (the map is small), so the blocks need not wait for one
+// another.
+__global__ void __launch_bounds__(256) plan_kernel(const CompactArgs A) {
+  __shared__ int s_sum[8][2];
+  __shared__ int s_scan[8];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int words = (int)((A.n_pages + 31) / 32);
+  const int w0 = blockIdx.x * 256;
+  int before = 0, total = 0;
+  for (int w = tid; w < words; w += 256) {
+    const int c = __popc(A.used[w]);
+    total += c;
+    before += w < w0 ? c : 0;
+  }
+  before = __reduce_add_sync(0xffffffffu, before);
+  total = __reduce_add_sync(0xffffffffu, total);
+  if (lane == 0) s_sum[warp][0] = before, s_sum[warp][1] = total;
+  const int w = w0 + tid;
+  const uint32_t bits = w < words ? A.used[w] : 0u;
+  int scan = __popc(bits);
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, scan, o);
+    if (lane >= o) scan += x;
+  }
+  if (lane == 31) s_scan[warp] = scan;
+  __syncthreads();
+  before = total = 0;
+#pragma unroll
+  for (int v = 0; v < 8; ++v) {
+    before += s_sum[v][0] + (v < warp ? s_scan[v] : 0);
+    total += s_sum[v][1];
+  }
+  before += scan - __popc(bits);  // used pages before this thread's word
+  // used pages below n_used, and so how many have to move
+  __shared__ int s_below[8];
+  int below = 0;
+  for (int v = tid; v <= total / 32 && v < words; v += 256) {
+    const uint32_t x = A.used[v];
+    below += __popc(v < total / 32 ? x : x & ((1u << (total & 31)) - 1u));
+  }
+  below = __reduce_add_sync(0xffffffffu, below);
+  if (lane == 0) s_below[warp] = below;
+  __syncthreads();
+  below = 0;
+#pragma unroll
+  for (int v = 0; v < 8; ++v) below += s_below[v];
+  if (blockIdx.x == 0 && tid == 0) {
+    *A.n_used = total;
+    *A.moves = total - below;
+  }
+  if (w >= words) return;
+  for (int i = 0; i < 32 && (int64_t)32 * w + i < A.n_pages; ++i) {
+    const int id = 32 * w + i;
+    const int ahead = before + __popc(bits & ((1u << i) - 1u));
+    const bool used = (bits >> i) & 1u;
+    int r = -1;
+    if (used && id >= total) {
+      r = ahead - below;
+      A.from[r] = id;
+    } else if (!used && id < total) {
+      A.to[id - ahead] = id;
+    }
+    A.rank[id] = r;
+  }
+}
+
+// Moves the pages, in pieces of `piece` 16-byte words (a warp each), and
+// rewrites the tables.  Sources lie at and above n_used, destinations below it
+// on unused pages: no piece is read after another has written it.
+__global__ void __launch_bounds__(256) move_kernel(const CompactArgs A, int piece) {
+  const int lane = threadIdx.x & 31;
+  const int64_t tid = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, threads = (int64_t)gridDim.x * blockDim.x;
+  const int64_t n = (int64_t)A.B * A.max_pages;
+  for (int64_t e = tid; e < n; e += threads) {
+    const int64_t b = e / A.max_pages;
+    const int p = (int)(e - b * A.max_pages);
+    int32_t id = live_entry(A, b, p);
+    if (id >= 0 && A.rank[id] >= 0) id = A.to[A.rank[id]];
+    A.tables_out[b * A.ld + p] = id;
+  }
+  const int64_t quads = A.L.page_words / 4, pieces = (quads + piece - 1) / piece;
+  const int64_t items = *A.moves * pieces;
+  for (int64_t it = tid >> 5; it < items; it += threads >> 5) {
+    const int64_t m = it / pieces, at = (it - m * pieces) * piece;
+    warp_copy(reinterpret_cast<uint4*>(A.pool + A.to[m] * A.L.page_words) + at,
+              reinterpret_cast<const uint4*>(A.pool + A.from[m] * A.L.page_words) + at, min64(piece, quads - at), lane);
+  }
+}
+
+size_t round256(size_t b) { return (b + 255) & ~(size_t)255; }
+
+}  // namespace
+}  // namespace paged
+}  // namespace tq
+
+extern "C" tq_status tq_paged_create(const tq_params* kp, const tq_params* vp, int layers, int Hkv, int page,
+                                     tq_paged** out) {
+  if (!out) return TQ_ERR_INVALID_ARG;
+  *out = nullptr;
+  if (layers < 1 || layers > 4096 || Hkv < 1 || Hkv > 1024 || page < 32 || page > 65536 || page % 32)
+    return TQ_ERR_INVALID_ARG;
+  if (!kp || !vp || kp->mode != TQ_MODE_PROD || (vp->mode != TQ_MODE_MSE && vp->mode != TQ_MODE_MSE_UNBIASED))
+    return TQ_ERR_INVALID_ARG;
+  if (kp->q.d != vp->q.d || kp->q.rot != vp->q.rot) return TQ_ERR_INVALID_ARG;
+  if (kp->q.rot != TQ_ROT_HADAMARD) return TQ_ERR_UNSUPPORTED;
+  tq_paged* pg = new (std::nothrow) tq_paged();
+  if (!pg) return TQ_ERR_INTERNAL;
+  pg->kq = kp->q;
+  pg->vq = vp->q;
+  tq::paged::Layout& L = pg->lay;
+  L.kw = kp->q.code_words;
+  L.sw = kp->q.sign_words;
+  L.nk = L.kw + L.sw;
+  L.gr = L.nk % 4 == 0 ? 4 : L.nk % 2 == 0 ? 2 : 1;
+  L.kv = vp->q.k;
+  L.dp = vp->q.d_pad;
+  L.r16 = kp->q.rnorm_f16;
+  L.o_kn = 32 * L.nk;
+  L.o_kr = L.o_kn + 32;
+  L.o_v = L.o_kr + (L.r16 ? 16 : 32);
+  L.o_vn = L.o_v + L.kv * L.dp;
+  L.words = L.o_vn + 32;
+  L.nb = page / 32;
+  L.layers = layers;
+  L.hkv = Hkv;
+  L.page = page;
+  L.page_words = (int64_t)layers * Hkv * L.nb * L.words;
+  *out = pg;
+  return TQ_OK;
+}
+
+extern "C" tq_status tq_paged_destroy(tq_paged* pg) {
+  delete pg;
+  return TQ_OK;
+}
+
+extern "C" tq_status tq_paged_info(const tq_paged* pg, int* block_words, int64_t* page_words) {
+  if (!pg) return TQ_ERR_INVALID_ARG;
+  if (block_words) *block_words = pg->lay.words;
+  if (page_words) *page_words = pg->lay.page_words;
+  return TQ_OK;
+}
+
+extern "C" tq_status tq_paged_append(const tq_paged* pg, uint32_t* pool, int64_t n_pages, int layer,
+                                     const uint32_t* kcodes, const uint32_t* ksigns, const float* knorms,
+                                     const float* krnorms, const uint32_t* vcodes, const float* vnorms, int64_t n_tok,
+                                     int B, const int32_t* cu, const int32_t* start, const int32_t* tables,
+                                     int64_t table_ld, int max_pages, void* stream) {
+  using namespace tq::paged;
+  if (!pg) return TQ_ERR_INVALID_ARG;
+  const Layout& L = pg->lay;
+  if (n_tok < 0 || n_tok > 0x7fffffffll || B < 0 || layer < 0 || layer >= L.layers || (!cu && n_tok != B))
+    return TQ_ERR_INVALID_ARG;
+  if (n_tok == 0 || B == 0) return TQ_OK;
+  if (bad_pool(L, pool, n_pages) || bad_table(L, tables, table_ld, max_pages)) return TQ_ERR_INVALID_ARG;
+  if (!kcodes || !ksigns || !knorms || !krnorms || !vcodes || !vnorms || !start || mis4(start) || mis4(cu))
+    return TQ_ERR_INVALID_ARG;
+  if (!al16(kcodes) || !al16(ksigns) || !al16(knorms) || !al16(krnorms) || !al16(vcodes) || !al16(vnorms))
+    return TQ_ERR_INVALID_ARG;
+  AppendArgs a = {L, {tables, table_ld, max_pages, n_pages}, pool, layer, kcodes, ksigns, vcodes, knorms, krnorms,
+                  vnorms, n_tok, B, cu, start};
+  const int64_t blocks = tq::ceil_div(n_tok * L.hkv, 4);
+  if (blocks > 0x7fffffffll) return TQ_ERR_UNSUPPORTED;
+  append_kernel<<<(unsigned)blocks, 128, 0, static_cast<cudaStream_t>(stream)>>>(a);
+  return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
+}
+
+extern "C" tq_status tq_paged_fork(const tq_paged* pg, uint32_t* pool, int64_t n_pages, int32_t* tables,
+                                   int64_t table_ld, int max_pages, int32_t* lens, int B, const int32_t* parents,
+                                   const int32_t* children, const int32_t* fresh, int n, void* stream) {
+  using namespace tq::paged;
+  if (!pg || n < 0 || B < 0) return TQ_ERR_INVALID_ARG;
+  const Layout& L = pg->lay;
+  if (n == 0) return TQ_OK;
+  if (bad_pool(L, pool, n_pages) || bad_table(L, tables, table_ld, max_pages)) return TQ_ERR_INVALID_ARG;
+  if (!lens || !parents || !children || !fresh || mis4(lens) || mis4(parents) || mis4(children) || mis4(fresh))
+    return TQ_ERR_INVALID_ARG;
+  ForkArgs a = {L, pool, n_pages, tables, table_ld, max_pages, lens, B, parents, children, fresh, n};
+  const int64_t items = (int64_t)n * L.layers * L.hkv;
+  const int64_t blocks = std::min<int64_t>(tq::ceil_div(items, 8), (int64_t)tq::sm_count() * 8);
+  fork_kernel<<<(unsigned)blocks, 256, 0, static_cast<cudaStream_t>(stream)>>>(a);
+  return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
+}
+
+extern "C" tq_status tq_paged_compact_workspace_size(int64_t n_pages, size_t* bytes) {
+  if (!bytes || n_pages < 1 || n_pages > 0x7fffffffll) return TQ_ERR_INVALID_ARG;
+  using tq::paged::round256;
+  *bytes = 256 + round256((size_t)(n_pages + 31) / 32 * 4) + 3 * round256((size_t)n_pages * 4);
+  return TQ_OK;
+}
+
+extern "C" tq_status tq_paged_compact(const tq_paged* pg, uint32_t* pool, int64_t n_pages, const int32_t* tables,
+                                      int32_t* tables_out, int64_t table_ld, int max_pages, const int32_t* lens,
+                                      int B, int32_t* n_used, void* ws, size_t ws_bytes, void* stream) {
+  using namespace tq::paged;
+  if (!pg || B < 0) return TQ_ERR_INVALID_ARG;
+  const Layout& L = pg->lay;
+  if (bad_pool(L, pool, n_pages) || !n_used || mis4(n_used)) return TQ_ERR_INVALID_ARG;
+  if (B > 0 && (bad_table(L, tables, table_ld, max_pages) || bad_table(L, tables_out, table_ld, max_pages) || !lens ||
+                mis4(lens)))
+    return TQ_ERR_INVALID_ARG;
+  size_t need = 0;
+  tq_paged_compact_workspace_size(n_pages, &need);
+  if (!ws || ws_bytes < need || !al256(ws)) return TQ_ERR_WORKSPACE;
+  char* w = static_cast<char*>(ws);
+  const size_t map = round256((size_t)(n_pages + 31) / 32 * 4), list = round256((size_t)n_pages * 4);
+  CompactArgs a = {L, pool, n_pages, tables, tables_out, table_ld, max_pages, lens, B, n_used,
+                   reinterpret_cast<uint32_t*>(w + 256), reinterpret_cast<int32_t*>(w + 256 + map),
+                   reinterpret_cast<int32_t*>(w + 256 + map + list), reinterpret_cast<int32_t*>(w + 256 + map + 2 * list),
+                   reinterpret_cast<int32_t*>(w)};
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (cudaMemsetAsync(a.used, 0, (size_t)(n_pages + 31) / 32 * 4, st) != cudaSuccess) return TQ_ERR_CUDA;
+  const int64_t entries = (int64_t)B * max_pages;
+  const int sms = tq::sm_count();
+  if (entries > 0)
+    mark_kernel<<<(unsigned)std::min<int64_t>(tq::ceil_div(entries, 256), (int64_t)sms * 8), 256, 0, st>>>(a);
+  plan_kernel<<<(unsigned)tq::ceil_div((n_pages + 31) / 32, 256), 256, 0, st>>>(a);
+  move_kernel<<<(unsigned)(sms * 8), 256, 0, st>>>(a, 512);
+  return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
+}

@@ -1,0 +1,68 @@
+// The paged compressed KV cache: its description and the places of a block
+// record's parts (include/tq.h, tq_paged_create).
+#pragma once
+
+#include <cstdint>
+
+#include "tq_internal.h"
+
+namespace tq {
+namespace paged {
+
+// Everything the kernels need to find a token: offsets in 32-bit words.
+struct Layout {
+  int kw, sw, nk;      // code words, sign words, key words of a token
+  int gr;              // words of a granule
+  int kv, dp;          // value bits, rotated dimension
+  int r16;             // residual norms are fp16
+  int o_kn, o_kr, o_v, o_vn;
+  int words;           // of a record
+  int nb;              // records of a page per layer and head
+  int layers, hkv, page;
+  int64_t page_words;
+};
+
+// One page table argument.
+struct Table {
+  const int32_t* rows;
+  int64_t ld;
+  int max_pages;
+  int64_t n_pages;
+};
+
+#ifdef __CUDACC__
+// First word of the record of block `blk` (32 tokens) of a sequence in layer
+// `layer`, head h; -1 in a hole.  64-bit: a pool can be larger than 2^31 words.
+__device__ __forceinline__ int64_t record_at(const Layout& L, const Table& t, int64_t b, int blk, int layer, int h) {
+  const int pi = blk / L.nb;
+  const int32_t id = t.rows[b * t.ld + pi];
+  if (id < 0 || id >= t.n_pages) return -1;
+  return id * L.page_words + ((int64_t)(layer * L.hkv + h) * L.nb + (blk - pi * L.nb)) * L.words;
+}
+__device__ __forceinline__ int key_word_at(const Layout& L, int t, int w) {
+  return (w / L.gr) * (32 * L.gr) + t * L.gr + w % L.gr;
+}
+__device__ __forceinline__ int clamp_len(int len, const Layout& L, int max_pages) {
+  const int top = max_pages * L.page;
+  return len < 0 ? 0 : len > top ? top : len;
+}
+#endif
+
+// Checks shared by the entry points (no handle's contents but the layout).
+inline bool bad_pool(const Layout& L, const void* pool, int64_t n_pages) {
+  return !pool || (reinterpret_cast<uintptr_t>(pool) & 15u) || n_pages < 1 || n_pages > 0x7fffffffll ||
+         L.page_words < 1;
+}
+inline bool bad_table(const Layout& L, const void* rows, int64_t ld, int max_pages) {
+  return !rows || (reinterpret_cast<uintptr_t>(rows) & 3u) || max_pages < 1 || ld < max_pages ||
+         (int64_t)max_pages * L.page > 0x7fffffffll;
+}
+inline bool mis4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
+
+}  // namespace paged
+}  // namespace tq
+
+struct tq_paged {
+  tq::QParams kq, vq;
+  tq::paged::Layout lay;
+};

@@ -1,0 +1,377 @@
+// tq_paged_attention: one query token per sequence over a paged compressed
+// cache (include/tq.h; the estimator and the rotated value average are those of
+// tq_decode_attention).  Three launches: the queries' rotation and sketch with
+// the split of the work, the attention over the segments, and the join.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "tq_paged_attn.cuh"
+
+namespace tq {
+namespace paged {
+namespace {
+
+inline bool al256(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
+
+// ---------------------------------------------------------------- queries
+
+// Block (b, h): q' = H D q / sqrt(d_pad) and u = S q' of the query heads of KV
+// head h, and, for h = 0, the blocks of the sequences before b.
+template <int A32>
+__global__ void __launch_bounds__(128) queries_kernel(const AttnArgs A, const QParams kq) {
+  constexpr int dp = 32 * A32;
+  __shared__ float qs[kMaxGroup][dp];
+  __shared__ long long s_sum[4];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int b = blockIdx.x / A.L.hkv, h = blockIdx.x % A.L.hkv;
+  if (h == 0) {
+    long long sum = 0;
+    for (int i = tid; i < b; i += 128) sum += (clamp_len(A.lens[i], A.L, A.tab.max_pages) + 31) / 32;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) s_sum[warp] = sum;
+    __syncthreads();
+    if (tid == 0) {
+      sum = s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3];
+      A.prefix[b] = sum;
+      if (b == A.B - 1) A.prefix[A.B] = sum + (clamp_len(A.lens[b], A.L, A.tab.max_pages) + 31) / 32;
+    }
+  }
+  const int64_t row0 = (int64_t)b * A.Hq + (int64_t)h * A.G;
+  for (int g = warp; g < A.G; g += 4) {
+    const int64_t at = b * A.q_ld + (int64_t)(h * A.G + g) * kq.d;
+    float v[A32];
+#pragma unroll
+    for (int a = 0; a < A32; ++a) {
+      const int j = 32 * a + lane;
+      v[a] = j < kq.d ? load_q(A, at + j) : 0.f;
+    }
+    apply_signs<A32>(v, kq.dmask, lane);
+    warp_fwht<A32>(v, lane);
+#pragma unroll
+    for (int a = 0; a < A32; ++a) {
+      v[a] *= kq.inv_sqrt_dpad;
+      qs[g][32 * a + lane] = v[a];
+      A.qrot[(row0 + g) * dp + 32 * a + lane] = v[a];
+    }
+  }
+  __syncthreads();
+  for (int i = tid; i < kq.m; i += 128) {
+    for (int g0 = 0; g0 < A.G; g0 += 4) {
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+      for (int j = 0; j < dp; ++j) {
+        const float s = kq.St[(int64_t)j * kq.m + i];
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          if (g0 + g < A.G) acc[g] = fmaf(s, qs[g0 + g][j], acc[g]);
+      }
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        if (g0 + g < A.G) A.u[(row0 + g0 + g) * kq.m + i] = acc[g];
+    }
+  }
+}
+
+// ---------------------------------------------------------------- attention, any shape
+
+// Index of token t's code for a coordinate from its value words.
+__device__ __forceinline__ int value_index(const uint32_t (&w)[4], int kv, int t) {
+  const int s = t & 3, i = t >> 2;
+  if (kv == 1) return (w[0] >> t) & 1;
+  if (kv == 4) {
+    const uint32_t x = s == 0 ? w[0] : s == 1 ? w[1] : s == 2 ? w[2] : w[3];
+    const int nib = (x >> (4 * i)) & 15;
+    return nib >= 8 ? 15 - nib : 8 + nib;
+  }
+  int idx = ((s < 2 ? w[0] : w[1]) >> (4 * i + 2 * (s & 1))) & 3;
+  if (kv == 3) idx |= ((w[2] >> ((t + 2) & 31)) & 1) << 2;
+  return idx;
+}
+
+// 128 threads: a warp's lanes are the tokens of a block for the scores of its
+// heads, a thread's coordinates tid + 128 c for the values.
+template <int NC>
+__global__ void __launch_bounds__(128) attention_any_kernel(const AttnArgs A, const QParams kq, const QParams vq) {
+  extern __shared__ float dyn[];
+  __shared__ float kc[kMaxLevels], vc[kMaxLevels];
+  __shared__ float p_s[32][kMaxGroup];
+  __shared__ float corr_s[kMaxGroup], m_s[kMaxGroup], l_s[kMaxGroup];
+  const Layout& L = A.L;
+  const int G = A.G, dp = L.dp, m = kq.m;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  float* qs = dyn;           // [G][dp]
+  float* us = dyn + G * dp;  // [G][m]
+  if (tid < kMaxLevels) {
+    kc[tid] = kq.centroids[tid];
+    vc[tid] = vq.centroids[tid];
+  }
+  const int64_t units = A.prefix[A.B] * L.hkv, share = share_of(A, units);
+  int64_t u0 = blockIdx.x * share;
+  const int64_t u1 = min64(units, u0 + share);
+  while (u0 < u1) {
+    const Segment sg = segment_at(A, u0, u1);
+    u0 += sg.end - sg.blk;
+    const int64_t row0 = (int64_t)sg.b * A.Hq + (int64_t)sg.h * G;
+    __syncthreads();
+    for (int e = tid; e < G * dp; e += 128) qs[e] = A.qrot[row0 * dp + e];
+    for (int e = tid; e < G * m; e += 128) us[e] = A.u[row0 * m + e];
+    if (tid < G) {
+      m_s[tid] = -INFINITY;
+      l_s[tid] = 0.f;
+    }
+    __syncthreads();
+    float o[kMaxGroup][NC];
+#pragma unroll
+    for (int g = 0; g < kMaxGroup; ++g)
+#pragma unroll
+      for (int c = 0; c < NC; ++c) o[g][c] = 0.f;
+    for (int blk = sg.blk; blk < sg.end; ++blk) {
+      const int64_t at = record_at(L, A.tab, sg.b, blk, A.layer, sg.h);
+      if (at < 0) continue;
+      const uint32_t* rec = A.pool + at;
+      const int nt = min(32, sg.len - 32 * blk);  // tokens of the block
+      const bool valid = lane < nt;
+      float am[4], aq[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) am[i] = aq[i] = 0.f;
+      float kn = 0.f, kr = 0.f, vn = 0.f;
+      if (valid) {
+        for (int w = 0; w < dp / 32; ++w) {
+          uint32_t pw[4];
+#pragma unroll
+          for (int p = 0; p < 4; ++p) pw[p] = p < kq.k ? rec[key_word_at(L, lane, p * (dp / 32) + w)] : 0u;
+          for (int i = 0; i < 32; ++i) {
+            int idx = 0;
+#pragma unroll
+            for (int p = 0; p < 4; ++p) idx |= (int)((pw[p] >> i) & 1u) << p;
+            const float c = kc[idx];
+#pragma unroll
+            for (int hh = 0; hh < 4; ++hh)
+              if (warp + 4 * hh < G) am[hh] = fmaf(qs[(warp + 4 * hh) * dp + 32 * w + i], c, am[hh]);
+          }
+        }
+        for (int w = 0; w < L.sw; ++w) {
+          const uint32_t x = rec[key_word_at(L, lane, L.kw + w)];
+          for (int i = 0; i < 32; ++i) {
+            const float sg1 = ((x >> i) & 1u) ? 1.f : -1.f;
+#pragma unroll
+            for (int hh = 0; hh < 4; ++hh)
+              if (warp + 4 * hh < G) aq[hh] = fmaf(us[(warp + 4 * hh) * m + 32 * w + i], sg1, aq[hh]);
+          }
+        }
+        kn = __uint_as_float(rec[L.o_kn + lane]);
+        kr = kq.kappa * get_rnorm(reinterpret_cast<const float*>(rec + L.o_kr), lane, L.r16);
+        vn = __uint_as_float(rec[L.o_vn + lane]);
+      }
+#pragma unroll
+      for (int hh = 0; hh < 4; ++hh) {
+        const int g = warp + 4 * hh;
+        if (g < G) {
+          const float x = valid ? A.scale * (kn * (am[hh] + kr * aq[hh])) : -INFINITY;
+          const float old = m_s[g], top = fmaxf(old, warp_max(x));
+          const float p = valid ? expf(x - top) : 0.f;
+          const float corr = expf(old - top);
+          const float sum = warp_sum(p);
+          p_s[lane][g] = p * vn;
+          if (lane == 0) {
+            corr_s[g] = corr;
+            m_s[g] = top;
+            l_s[g] = l_s[g] * corr + sum;
+          }
+        }
+      }
+      __syncthreads();
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        const int j = tid + 128 * c;
+        if (j >= dp) continue;
+        uint32_t pw[4];
+#pragma unroll
+        for (int p = 0; p < 4; ++p) pw[p] = p < L.kv ? rec[L.o_v + p * dp + j] : 0u;
+#pragma unroll
+        for (int g = 0; g < kMaxGroup; ++g)
+          if (g < G) o[g][c] *= corr_s[g];
+        for (int t = 0; t < nt; ++t) {
+          const float v = vc[value_index(pw, L.kv, t)];
+#pragma unroll
+          for (int g = 0; g < kMaxGroup; ++g)
+            if (g < G) o[g][c] = fmaf(p_s[t][g], v, o[g][c]);
+        }
+      }
+      __syncthreads();
+    }
+    const int64_t bh = (int64_t)sg.b * L.hkv + sg.h;
+#pragma unroll
+    for (int g = 0; g < kMaxGroup; ++g) {
+      if (g < G) {
+        float* pp = slot_of(A, bh, blockIdx.x, g);
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+          if (tid + 128 * c < dp) pp[2 + tid + 128 * c] = o[g][c];
+        if (tid == 0) {
+          pp[0] = m_s[g];
+          pp[1] = l_s[g];
+        }
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- join
+
+// Block (b, query head), four warps: the parts' maximum, then warp w sums parts
+// w, w + 4, ... and warp 0 adds the four sums, rotates back and stores.
+template <int A32>
+__global__ void __launch_bounds__(128) join_kernel(const AttnArgs A, const QParams vq) {
+  constexpr int dp = 32 * A32;
+  __shared__ float sm[4], sl[4], sv[4][dp];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int b = blockIdx.x / A.Hq, hq = blockIdx.x % A.Hq;
+  const int h = hq / A.G, g = hq % A.G;
+  const int hkv = A.L.hkv;
+  const int64_t p0 = A.prefix[b];
+  const int64_t n = A.prefix[b + 1] - p0;
+  const int64_t share = share_of(A, A.prefix[A.B] * hkv);
+  const int64_t s0 = hkv * p0 + h * n, bh = (int64_t)b * hkv + h;
+  // parts c0 .. c1; none of an empty sequence
+  const int c0 = (int)(s0 / share), c1 = n ? (int)((s0 + n - 1) / share) : c0 - 1;
+  float top = -INFINITY;
+  for (int c = c0 + tid; c <= c1; c += 128) top = fmaxf(top, slot_of(A, bh, c, g)[0]);
+  top = warp_max(top);
+  if (lane == 0) sm[warp] = top;
+  __syncthreads();
+  top = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
+  float l = 0.f, v[A32];
+#pragma unroll
+  for (int a = 0; a < A32; ++a) v[a] = 0.f;
+  for (int c = c0 + warp; c <= c1; c += 4) {
+    const float* pp = slot_of(A, bh, c, g);
+    if (pp[1] == 0.f) continue;  // holes only (a NaN sum is not zero: it goes on)
+    const float e = expf(pp[0] - top);
+    l = fmaf(e, pp[1], l);
+#pragma unroll
+    for (int a = 0; a < A32; ++a) v[a] = fmaf(e, pp[2 + 32 * a + lane], v[a]);
+  }
+  if (lane == 0) sl[warp] = l;
+#pragma unroll
+  for (int a = 0; a < A32; ++a) sv[warp][32 * a + lane] = v[a];
+  __syncthreads();
+  if (warp != 0) return;
+  l = sl[0] + sl[1] + sl[2] + sl[3];
+#pragma unroll
+  for (int a = 0; a < A32; ++a)
+    v[a] = sv[0][32 * a + lane] + sv[1][32 * a + lane] + sv[2][32 * a + lane] + sv[3][32 * a + lane];
+  // no token: zeros; (a NaN sum is not zero and stays one)
+  const float inv = l == 0.f ? 0.f : vq.inv_sqrt_dpad / l;
+  warp_fwht<A32>(v, lane);
+  apply_signs<A32>(v, vq.dmask, lane);
+#pragma unroll
+  for (int a = 0; a < A32; ++a) {
+    const int j = 32 * a + lane;
+    if (j < vq.d) store_out(A, ((int64_t)b * A.Hq + hq) * vq.d + j, v[a] * inv);
+  }
+  if (lane == 0 && A.lse) A.lse[(int64_t)b * A.Hq + hq] = l == 0.f ? -INFINITY : top + logf(l);
+}
+
+int attention_ctas() { return sm_count() * 4; }
+
+struct Sizes {
+  size_t prefix, qrot, u, part;
+  size_t all() const { return prefix + qrot + u + part; }
+};
+
+size_t round256(size_t b) { return (b + 255) & ~(size_t)255; }
+
+Sizes sizes_of(const tq_paged* pg, int B, int Hq) {
+  const Layout& L = pg->lay;
+  const size_t heads = (size_t)B * Hq;
+  Sizes s;
+  s.prefix = round256(((size_t)B + 1) * 8);
+  s.qrot = round256(heads * L.dp * 4);
+  s.u = round256(heads * pg->kq.m * 4);
+  s.part = round256(((size_t)B * L.hkv + attention_ctas()) * (Hq / L.hkv) * (L.dp + 2) * 4);
+  return s;
+}
+
+template <int A32>
+cudaError_t run(const AttnArgs& a, const tq_paged* pg, cudaStream_t st) {
+  queries_kernel<A32><<<(unsigned)(a.B * a.L.hkv), 128, 0, st>>>(a, pg->kq);
+  constexpr int NC = A32 > 4 ? 2 : 1;
+  const size_t smem = (size_t)a.G * (a.L.dp + pg->kq.m) * sizeof(float);
+  // function attributes are per device: set on every call (a cheap host call)
+  const cudaError_t e = cudaFuncSetAttribute(attention_any_kernel<NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  attention_any_kernel<NC><<<a.ctas, 128, smem, st>>>(a, pg->kq, pg->vq);
+  join_kernel<A32><<<(unsigned)(a.B * a.Hq), 128, 0, st>>>(a, pg->vq);
+  return cudaGetLastError();
+}
+
+// What does not fit the kernels' shared memory: the queries of a group.
+bool too_wide(const tq_paged* pg, int G) { return (size_t)G * (pg->lay.dp + pg->kq.m) * sizeof(float) > 200 * 1024; }
+
+}  // namespace
+}  // namespace paged
+}  // namespace tq
+
+extern "C" tq_status tq_paged_attention_workspace_size(const tq_paged* pg, int B, int Hq, size_t* bytes) {
+  using namespace tq::paged;
+  if (!pg || !bytes || B < 0 || B > (1 << 20) || Hq < pg->lay.hkv || Hq % pg->lay.hkv) return TQ_ERR_INVALID_ARG;
+  if (Hq / pg->lay.hkv > kMaxGroup || too_wide(pg, Hq / pg->lay.hkv)) return TQ_ERR_UNSUPPORTED;
+  *bytes = B == 0 ? 0 : sizes_of(pg, B, Hq).all();
+  return TQ_OK;
+}
+
+extern "C" tq_status tq_paged_attention(const tq_paged* pg, const void* q, tq_dtype dt, int64_t q_ld, int B, int Hq,
+                                        const uint32_t* pool, int64_t n_pages, int layer, const int32_t* lens,
+                                        const int32_t* tables, int64_t table_ld, int max_pages, float scale, void* out,
+                                        float* lse, void* ws, size_t ws_bytes, void* stream) {
+  using namespace tq::paged;
+  size_t need = 0;
+  const tq_status s = tq_paged_attention_workspace_size(pg, B, Hq, &need);
+  if (s != TQ_OK) return s;
+  const Layout& L = pg->lay;
+  if ((dt != TQ_F32 && dt != TQ_F16 && dt != TQ_BF16) || layer < 0 || layer >= L.layers) return TQ_ERR_INVALID_ARG;
+  if (B == 0) return TQ_OK;
+  if (bad_pool(L, pool, n_pages) || bad_table(L, tables, table_ld, max_pages)) return TQ_ERR_INVALID_ARG;
+  const uintptr_t esz = dt == TQ_F32 ? 4 : 2;
+  if (!q || !out || !lens || mis4(lens) || mis4(lse) || reinterpret_cast<uintptr_t>(q) % esz ||
+      reinterpret_cast<uintptr_t>(out) % esz || (B > 1 && q_ld < (int64_t)Hq * pg->kq.d))
+    return TQ_ERR_INVALID_ARG;
+  if ((int64_t)B * Hq > 0x7fffffffll) return TQ_ERR_UNSUPPORTED;
+  if (!ws || ws_bytes < need || !al256(ws)) return TQ_ERR_WORKSPACE;
+  const Sizes z = sizes_of(pg, B, Hq);
+  char* w = static_cast<char*>(ws);
+  AttnArgs a = {};
+  a.L = L;
+  a.tab = {tables, table_ld, max_pages, n_pages};
+  a.pool = pool;
+  a.layer = layer;
+  a.lens = lens;
+  a.B = B;
+  a.Hq = Hq;
+  a.G = Hq / L.hkv;
+  a.scale = scale;
+  a.q = q;
+  a.dt = dt;
+  a.q_ld = q_ld;
+  a.out = out;
+  a.lse = lse;
+  a.ctas = attention_ctas();
+  a.prefix = reinterpret_cast<int64_t*>(w);
+  a.qrot = reinterpret_cast<float*>(w + z.prefix);
+  a.u = reinterpret_cast<float*>(w + z.prefix + z.qrot);
+  a.part = reinterpret_cast<float*>(w + z.prefix + z.qrot + z.u);
+  a.err = tq::error_word();
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  switch (L.dp / 32) {
+    case 1: e = run<1>(a, pg, st); break;
+    case 2: e = run<2>(a, pg, st); break;
+    case 4: e = run<4>(a, pg, st); break;
+    default: e = run<8>(a, pg, st); break;
+  }
+  return e == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
+}
