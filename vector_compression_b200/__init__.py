@@ -8,6 +8,7 @@ patterns of the C ABI.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 from typing import Optional
 
@@ -27,6 +28,9 @@ __all__ = [
     "F32", "F16", "BF16", "LAYOUT_ROW", "LAYOUT_BLOCK32", "MODE_MSE", "MODE_PROD", "MODE_MSE_UNBIASED",
     "STORE_RNORM_F16", "ROT_HADAMARD", "ROT_DENSE", "ROPE_PLAIN", "ROPE_LINEAR", "ROPE_BANDS", "ROPE_YARN",
 ]
+
+
+_nothing = contextlib.nullcontext()
 
 
 def _torch():
@@ -349,29 +353,52 @@ class TQRope:
             pass
 
 
-def _on(device, *tensors):
-    """The device that every given tensor is on, and an int32/int64/float check left to the callers."""
-    for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"a tensor on {t.device} beside one on {device}")
-    if device.type != "cuda":
-        raise ValueError(f"tensors on {device}: a CUDA device is needed")
-    return _torch().cuda.device(device)
-
-
-def _int32(name, t, shape):
+def _call(name, device, stream, *args):
+    """Call an entry point with the device current and the stream last; raises on a bad status."""
     torch = _torch()
-    if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous int32 {tuple(shape)}")
+    fn = getattr(L.lib(), name)
+    i = device.index
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(i)
+    else:
+        stream = stream.cuda_stream
+    if torch.cuda.current_device() == i:
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(i):
+            status = fn(*args, stream)
+    if status:
+        L.check(name, status)
 
 
-def _heads(name, x, n, d, dtype):
-    """Token and head strides of a [n, heads, d] tensor whose last dimension is contiguous."""
-    if x.dim() != 3 or x.shape[0] != n or x.shape[2] != d or x.dtype != dtype:
-        raise ValueError(f"{name} must be [{n}, heads, {d}] {dtype}")
-    if x.numel() and d > 1 and x.stride(2) != 1:
+def _one_device(*tensors):
+    """The CUDA device that every given tensor is on."""
+    at = -2
+    for t in tensors:
+        if t is not None:
+            i = t.get_device()
+            if i != at and at != -2:
+                raise ValueError("the tensors are on different devices")
+            at = i
+    if at < 0:
+        raise ValueError("a CUDA device is needed")
+    return tensors[0].device
+
+
+def _is(name, t, dtype, shape):
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {dtype} {tuple(shape)}")
+    return t.data_ptr()
+
+
+def _heads(name, x, n, heads, d, dtype):
+    """Pointer, token and head strides of a [n, heads, d] tensor whose last dimension is contiguous."""
+    if x.dtype != dtype or x.shape != (n, heads, d):
+        raise ValueError(f"{name} must be [{n}, {heads}, {d}] {dtype}")
+    st, sh, sd = x.stride()
+    if sd != 1 and d > 1 and n * heads:
         raise ValueError(f"the last dimension of {name} must be contiguous")
-    return x.stride(0), x.stride(1)
+    return x.data_ptr(), st, sh
 
 
 def tq_qk_norm_rope(rope: Optional[TQRope], q, k, pos=None, wq=None, wk=None, eps: float = 1e-6,
@@ -382,30 +409,23 @@ def tq_qk_norm_rope(rope: Optional[TQRope], q, k, pos=None, wq=None, wk=None, ep
     k_out); the outputs may be the inputs."""
     torch = _torch()
     n, Hq, d = q.shape
-    qs = _heads("q", q, n, d, q.dtype)
+    dt = q.dtype
+    device = _one_device(q, k, pos, wq, wk, q_out, k_out)
     if q_out is None:
-        q_out = torch.empty((n, Hq, d), dtype=q.dtype, device=q.device)
-    qos = _heads("q_out", q_out, n, d, q.dtype)
-    Hkv, ks, kos = 0, (0, 0), (0, 0)
+        q_out = torch.empty((n, Hq, d), dtype=dt, device=device)
+    qi, qo = _heads("q", q, n, Hq, d, dt), _heads("q_out", q_out, n, Hq, d, dt)
+    Hkv, ki, ko = 0, (None, 0, 0), (None, 0, 0)
     if k is not None:
-        ks, Hkv = _heads("k", k, n, d, q.dtype), k.shape[1]
+        Hkv = k.shape[1]
         if k_out is None:
-            k_out = torch.empty((n, Hkv, d), dtype=q.dtype, device=q.device)
-        kos = _heads("k_out", k_out, n, d, q.dtype)
-        if k_out.shape != k.shape:
-            raise ValueError("k_out must have the shape of k")
-    if q_out.shape != q.shape:
-        raise ValueError("q_out must have the shape of q")
-    if rope is not None and (pos is None or pos.dtype != torch.int64 or tuple(pos.shape) != (n,) or
-                             not pos.is_contiguous()):
-        raise ValueError(f"pos must be contiguous int64 [{n}]")
-    for name, w in (("wq", wq), ("wk", wk)):
-        if w is not None and (w.dtype != q.dtype or tuple(w.shape) != (d,) or not w.is_contiguous()):
-            raise ValueError(f"{name} must be contiguous [{d}] {q.dtype}")
-    with _on(q.device, k, pos, wq, wk, q_out, k_out):
-        L.check("tq_qk_norm_rope", L.lib().tq_qk_norm_rope(
-            None if rope is None else rope.handle, _dtype_code(q), n, d, Hq, _ptr(q), *qs, Hkv, _ptr(k), *ks,
-            _ptr(pos), _ptr(wq), _ptr(wk), eps, _ptr(q_out), *qos, _ptr(k_out), *kos, _stream(stream)))
+            k_out = torch.empty((n, Hkv, d), dtype=dt, device=device)
+        ki, ko = _heads("k", k, n, Hkv, d, dt), _heads("k_out", k_out, n, Hkv, d, dt)
+    if rope is not None and pos is None:
+        raise ValueError("a rotation needs positions")
+    _call("tq_qk_norm_rope", device, stream, None if rope is None else rope.handle, _dtype_code(q), n, d, Hq, *qi,
+          Hkv, *ki, None if pos is None else _is("pos", pos, torch.int64, (n,)),
+          None if wq is None else _is("wq", wq, dt, (d,)), None if wk is None else _is("wk", wk, dt, (d,)), eps,
+          *qo, *ko)
     return q_out, k_out
 
 
@@ -419,6 +439,7 @@ class TQPaged:
         L.check("tq_paged_info", L.lib().tq_paged_info(self._h, C.byref(bw), C.byref(pw)))
         self.kp, self.vp, self.layers, self.hkv, self.page = kp, vp, layers, hkv, page
         self.block_words, self.page_words = bw.value, pw.value
+        self._rnorm = getattr(_torch(), kp.rnorm_dtype)
 
     @property
     def handle(self):
@@ -442,17 +463,26 @@ class TQPaged:
 
 
 def _pool(pg, pool):
-    torch = _torch()
-    if pool.dtype != torch.int32 or pool.dim() != 2 or pool.shape[1] != pg.page_words or not pool.is_contiguous():
+    if pool.dtype != _torch().int32 or pool.dim() != 2 or pool.shape[1] != pg.page_words or not pool.is_contiguous():
         raise ValueError(f"pool must be contiguous int32 [n_pages, {pg.page_words}]")
-    return _ptr(pool), pool.shape[0]
+    return pool.data_ptr(), pool.shape[0]
 
 
 def _table(name, t, B):
-    torch = _torch()
-    if t.dtype != torch.int32 or t.dim() != 2 or t.shape[0] != B or (t.numel() and t.stride(1) != 1):
-        raise ValueError(f"{name} must be int32 [{B}, max_pages] with contiguous rows")
-    return _ptr(t), max(t.stride(0), t.shape[1]) if B > 1 else t.shape[1], t.shape[1]
+    """Pointer, row stride and width of a page table (rows contiguous, any stride between them)."""
+    if t.dtype != _torch().int32 or t.dim() != 2 or t.shape[0] != B:
+        raise ValueError(f"{name} must be int32 [{B}, max_pages]")
+    width = t.shape[1]
+    ld, one = t.stride()
+    if B and (one != 1 and width > 1 or B > 1 and ld < width):
+        raise ValueError(f"the rows of {name} must be contiguous and apart")
+    return t.data_ptr(), max(ld, width), width
+
+
+def _encoded(name, t, dtype, n):
+    if t.dtype != dtype or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be {n} contiguous {dtype}")
+    return t.data_ptr()
 
 
 def tq_paged_append(pg: TQPaged, pool, layer: int, keys, values, start, tables, cu=None, stream=None):
@@ -462,28 +492,23 @@ def tq_paged_append(pg: TQPaged, pool, layer: int, keys, values, start, tables, 
     cu[b + 1] - 1 (cu int32 [B + 1]; None: token b) go to the positions from
     start[b] (int32 [B]) on of sequence b, whose pages are tables[b]."""
     torch = _torch()
-    B = start.shape[0]
+    i32, f32 = torch.int32, torch.float32
     kcodes, ksigns, knorms, krnorms = keys
     vcodes, vnorms = values
-    rows = knorms.numel()
+    B, rows = start.shape[0], knorms.numel()
     n_tok = rows // pg.hkv
     if rows != n_tok * pg.hkv:
         raise ValueError(f"{rows} rows are no multiple of {pg.hkv} heads")
-    words = (("key codes", kcodes, pg.kp.code_words, torch.int32), ("signs", ksigns, pg.kp.sign_words, torch.int32),
-             ("key norms", knorms, 1, torch.float32), ("residual norms", krnorms, 1, getattr(torch, pg.kp.rnorm_dtype)),
-             ("value codes", vcodes, pg.vp.code_words, torch.int32), ("value norms", vnorms, 1, torch.float32))
-    for name, t, w, dt in words:
-        if t.dtype != dt or t.numel() != rows * w or not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous {dt} with {w} words for each of {rows} rows")
-    _int32("start", start, (B,))
-    if cu is not None:
-        _int32("cu", cu, (B + 1,))
-    elif n_tok != B:
+    if cu is None and n_tok != B:
         raise ValueError(f"{n_tok} tokens for {B} sequences need cu")
-    with _on(pool.device, kcodes, ksigns, knorms, krnorms, vcodes, vnorms, start, tables, cu):
-        L.check("tq_paged_append", L.lib().tq_paged_append(
-            pg.handle, *_pool(pg, pool), layer, _ptr(kcodes), _ptr(ksigns), _ptr(knorms), _ptr(krnorms),
-            _ptr(vcodes), _ptr(vnorms), n_tok, B, _ptr(cu), _ptr(start), *_table("tables", tables, B), _stream(stream)))
+    device = _one_device(pool, kcodes, ksigns, knorms, krnorms, vcodes, vnorms, start, tables, cu)
+    _call("tq_paged_append", device, stream, pg.handle, *_pool(pg, pool), layer,
+          _encoded("key codes", kcodes, i32, rows * pg.kp.code_words),
+          _encoded("key signs", ksigns, i32, rows * pg.kp.sign_words), _encoded("key norms", knorms, f32, rows),
+          _encoded("residual norms", krnorms, pg._rnorm, rows),
+          _encoded("value codes", vcodes, i32, rows * pg.vp.code_words), _encoded("value norms", vnorms, f32, rows),
+          n_tok, B, None if cu is None else _is("cu", cu, i32, (B + 1,)), _is("start", start, i32, (B,)),
+          *_table("tables", tables, B))
 
 
 def tq_paged_attention_workspace_size(pg: TQPaged, B: int, Hq: int) -> int:
@@ -503,24 +528,22 @@ def tq_paged_attention(pg: TQPaged, q, pool, layer: int, lens, tables, scale: fl
     B, Hq, d = q.shape
     if d != pg.kp.d:
         raise ValueError(f"last dimension {d} != d {pg.kp.d}")
-    if q.numel() and (q.stride(2) != 1 or q.stride(1) != d or (B > 1 and q.stride(0) < Hq * d)):
+    sb, sh, sd = q.stride()
+    if (sd != 1 or sh != d or (B > 1 and sb < Hq * d)) and q.numel():
         q = q.contiguous()
-    _int32("lens", lens, (B,))
+        sb = Hq * d
+    device = _one_device(q, pool, lens, tables, out, lse, ws)
     if out is None:
-        out = torch.empty((B, Hq, d), dtype=q.dtype, device=q.device)
-    if out.dtype != q.dtype or tuple(out.shape) != (B, Hq, d) or not out.is_contiguous():
-        raise ValueError(f"out must be contiguous [{B}, {Hq}, {d}] {q.dtype}")
+        out = torch.empty((B, Hq, d), dtype=q.dtype, device=device)
     if lse is None and want_lse:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
-    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (B, Hq) or not lse.is_contiguous()):
-        raise ValueError(f"lse must be contiguous float32 [{B}, {Hq}]")
-    with _on(q.device, pool, lens, tables, out, lse, ws):
-        if ws is None:
-            ws = _ws(tq_paged_attention_workspace_size(pg, B, Hq), q.device)
-        L.check("tq_paged_attention", L.lib().tq_paged_attention(
-            pg.handle, _ptr(q), _dtype_code(q), max(q.stride(0), Hq * d), B, Hq, *_pool(pg, pool), layer, _ptr(lens),
-            *_table("tables", tables, B), float(scale), _ptr(out), _ptr(lse), _ptr(ws),
-            0 if ws is None else ws.numel(), _stream(stream)))
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=device)
+    if ws is None:
+        with torch.cuda.device(device) if torch.cuda.current_device() != device.index else _nothing:
+            ws = _ws(tq_paged_attention_workspace_size(pg, B, Hq), device)
+    _call("tq_paged_attention", device, stream, pg.handle, q.data_ptr(), _dtype_code(q), max(sb, Hq * d), B, Hq,
+          *_pool(pg, pool), layer, _is("lens", lens, torch.int32, (B,)), *_table("tables", tables, B), scale,
+          _is("out", out, q.dtype, (B, Hq, d)), None if lse is None else _is("lse", lse, torch.float32, (B, Hq)),
+          None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel() * ws.element_size())
     return (out, lse) if want_lse else out
 
 
@@ -528,14 +551,12 @@ def tq_paged_fork(pg: TQPaged, pool, tables, lens, parents, children, fresh, str
     """Make sequences children[i] copies of parents[i]: table rows, lengths and
     (into page fresh[i]) the partly filled last page.  All int32; tables and
     lens are updated in place."""
+    i32 = _torch().int32
     B, n = lens.shape[0], parents.shape[0]
-    _int32("lens", lens, (B,))
-    for name, t in (("parents", parents), ("children", children), ("fresh", fresh)):
-        _int32(name, t, (n,))
-    with _on(pool.device, tables, lens, parents, children, fresh):
-        L.check("tq_paged_fork", L.lib().tq_paged_fork(
-            pg.handle, *_pool(pg, pool), *_table("tables", tables, B), _ptr(lens), B, _ptr(parents), _ptr(children),
-            _ptr(fresh), n, _stream(stream)))
+    device = _one_device(pool, tables, lens, parents, children, fresh)
+    _call("tq_paged_fork", device, stream, pg.handle, *_pool(pg, pool), *_table("tables", tables, B),
+          _is("lens", lens, i32, (B,)), B, _is("parents", parents, i32, (n,)), _is("children", children, i32, (n,)),
+          _is("fresh", fresh, i32, (n,)), n)
 
 
 def tq_paged_compact_workspace_size(n_pages: int) -> int:
@@ -550,21 +571,19 @@ def tq_paged_compact(pg: TQPaged, pool, tables, lens, tables_out=None, n_used=No
     the device): pages n_used and behind are free."""
     torch = _torch()
     B = lens.shape[0]
-    _int32("lens", lens, (B,))
+    device = _one_device(pool, tables, lens, tables_out, n_used, ws)
     if tables_out is None:
         tables_out = tables
-    if n_used is None:
-        n_used = torch.empty(1, dtype=torch.int32, device=pool.device)
-    _int32("n_used", n_used, (1,))
-    if tables_out.shape != tables.shape or tables_out.stride() != tables.stride():
+    elif tables_out.shape != tables.shape or tables_out.stride() != tables.stride():
         raise ValueError("tables_out must have the shape and strides of tables")
-    tab = _table("tables", tables, B)
-    with _on(pool.device, tables, tables_out, lens, n_used, ws):
-        if ws is None:
-            ws = _ws(tq_paged_compact_workspace_size(pool.shape[0]), pool.device)
-        L.check("tq_paged_compact", L.lib().tq_paged_compact(
-            pg.handle, *_pool(pg, pool), tab[0], _table("tables_out", tables_out, B)[0], *tab[1:], _ptr(lens), B,
-            _ptr(n_used), _ptr(ws), ws.numel(), _stream(stream)))
+    if n_used is None:
+        n_used = torch.empty(1, dtype=torch.int32, device=device)
+    if ws is None:
+        ws = _ws(tq_paged_compact_workspace_size(pool.shape[0]), device)
+    tab, ld, width = _table("tables", tables, B)
+    _call("tq_paged_compact", device, stream, pg.handle, *_pool(pg, pool), tab,
+          _table("tables_out", tables_out, B)[0], ld, width, _is("lens", lens, torch.int32, (B,)), B,
+          _is("n_used", n_used, torch.int32, (1,)), ws.data_ptr(), ws.numel() * ws.element_size())
     return n_used
 
 
