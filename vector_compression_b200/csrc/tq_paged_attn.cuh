@@ -1,13 +1,16 @@
-// What the two kernels of tq_paged_attention share: the split of the work, and
-// the join of its parts.
+// What the kernels of tq_paged_attention share: the split of the work, and the
+// join of its parts.
 //
-// The blocks of 32 tokens of all sequences and KV heads, in the order (sequence,
-// head, block), are one line of U units, cut into equal shares, one per CTA,
-// whatever the sequences' lengths; so a long sequence is spread over many CTAs
-// and a CTA may hold several short ones.  What a CTA has of one (sequence, head)
-// is a segment; it leaves the partial (m, l, o) of each of its segments in the
-// workspace.  Segment (bh, CTA c) has slot bh + c: from one segment to the next
-// bh or c or both grow, so no two share a slot.
+// The query heads of a KV head are taken in groups of at most `gh`; a KV head
+// with its group is a virtual head, `hv` per sequence.  The blocks of 32 tokens
+// of all sequences and virtual heads, in the order (sequence, virtual head,
+// block), are one line of U units, cut into equal shares, one per worker (a
+// warp or a CTA), whatever the sequences' lengths; so a long sequence is spread
+// over many workers and a worker may hold several short ones.  What a worker
+// has of one (sequence, virtual head) is a segment; it leaves the partial
+// (m, l, o) of each of its segments in the workspace, m as a power of two's
+// exponent.  Segment (bh, worker c) has slot bh + c: from one segment to the
+// next bh or c or both grow, so no two share a slot.
 #pragma once
 
 #include "tq_device.cuh"
@@ -16,8 +19,9 @@
 namespace tq {
 namespace paged {
 
-constexpr int kMinShare = 4;  // blocks: below 128 tokens a CTA's setup outweighs its work
+constexpr int kMinShare = 4;  // blocks: what a warp's value pass takes at a time
 constexpr int kMaxGroup = 16; // query heads per KV head
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct AttnArgs {
   Layout L;
@@ -26,54 +30,60 @@ struct AttnArgs {
   int layer;
   const int32_t* lens;
   int B, Hq, G;
-  float scale;
+  int hv, gh;            // virtual heads per sequence, query heads of one
+  float scale2;          // scale log2(e)
   const void* q;
   int dt;
   int64_t q_ld;
   void* out;
   float* lse;
-  int ctas;              // of the main kernel
+  int workers;           // of the main kernel
   int64_t* prefix;       // [B + 1]: blocks of the sequences before b
-  float* qrot;           // [B * Hq][d_pad]
+  float* qrot;           // [B * Hq][d_pad] (the kernel for any shape)
   float* u;              // [B * Hq][m]
-  float* part;           // [slots][G][d_pad + 2]
+  uint32_t* frag;        // [B * hv] query images (the tensor-core kernel)
+  int frag_words;        // of one
+  float* part;           // [slots][gh][4 + d_pad]: m, l, -, -, o
   unsigned* err;
 };
 
 __device__ __forceinline__ int64_t share_of(const AttnArgs& A, int64_t units) {
-  const int64_t s = (units + A.ctas - 1) / A.ctas;
+  const int64_t s = (units + A.workers - 1) / A.workers;
   return s < kMinShare ? kMinShare : s;
 }
 
 struct Segment {
-  int b, h, blk, end;  // blocks [blk, end) of (b, h)
+  int b, h, blk, end;  // blocks [blk, end) of (sequence, virtual head)
   int len;             // tokens of the sequence
 };
 
-// The segment that unit u0 begins, cut at u1.
-__device__ __forceinline__ Segment segment_at(const AttnArgs& A, int64_t u0, int64_t u1) {
-  const int hkv = A.L.hkv;
-  const int64_t x = u0 / hkv;
-  int lo = 0, hi = A.B;  // prefix[lo] <= x < prefix[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (A.prefix[mid] <= x) lo = mid;
-    else hi = mid;
+// The segment that unit u0 begins, cut at u1; called by a whole warp.
+__device__ __forceinline__ Segment segment_at(const AttnArgs& A, int64_t u0, int64_t u1, int lane) {
+  const int64_t x = u0 / A.hv;
+  int lo = 0, n = A.B;  // the last b with prefix[b] <= x is in [lo, lo + n)
+  while (n > 1) {
+    const int step = (n + 31) / 32;
+    const bool le = lane * step < n && A.prefix[lo + lane * step] <= x;
+    const int last = __popc(__ballot_sync(0xffffffffu, le)) - 1;
+    lo += last * step;
+    n = min(step, n - last * step);
   }
   const int64_t p = A.prefix[lo];
-  const int n = (int)(A.prefix[lo + 1] - p);
-  const int64_t rel = u0 - hkv * p;
+  const int nb = (int)(A.prefix[lo + 1] - p);
+  const int64_t rel = u0 - A.hv * p;
   Segment s;
   s.b = lo;
-  s.h = (int)(rel / n);
-  s.blk = (int)(rel - (int64_t)s.h * n);
-  s.end = (int)min64(n, s.blk + (u1 - u0));
+  s.h = (int)(rel / nb);
+  s.blk = (int)(rel - (int64_t)s.h * nb);
+  s.end = (int)min64(nb, s.blk + (u1 - u0));
   s.len = clamp_len(A.lens[lo], A.L, A.tab.max_pages);
   return s;
 }
 
-__device__ __forceinline__ float* slot_of(const AttnArgs& A, int64_t bh, int c, int head) {
-  return A.part + ((bh + c) * A.G + head) * (int64_t)(A.L.dp + 2);
+__host__ __device__ __forceinline__ int part_row(int dp) { return dp + 4; }  // 16-byte rows
+
+__device__ __forceinline__ float* slot_of(const AttnArgs& A, int64_t bh, int worker, int head) {
+  return A.part + ((bh + worker) * A.gh + head) * (int64_t)part_row(A.L.dp);
 }
 
 __device__ __forceinline__ float load_q(const AttnArgs& A, int64_t i) {
@@ -86,6 +96,46 @@ __device__ __forceinline__ void store_out(const AttnArgs& A, int64_t i, float v)
   else if (A.dt == TQ_F16) static_cast<__half*>(A.out)[i] = __float2half_rn(v);
   else static_cast<__nv_bfloat16*>(A.out)[i] = __float2bfloat16_rn(v);
 }
+
+// Launches that depend on the one before them may be set up early: a kernel
+// waits here before it reads what that one wrote ...
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// ... and says here that its successor may be set up.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <typename... Ps, typename... As>
+cudaError_t launch_after(void (*kern)(Ps...), dim3 grid, int threads, size_t smem, cudaStream_t st, As... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at = {};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+// The tensor-core kernel (tq_paged_attn_tc.cuh): what it needs to know of a
+// shape, and its launch.  ctas == 0: not a shape of it.
+struct TcShape {
+  int ctas_per_sm = 0;
+  int warps;       // of a CTA
+  int nt;          // tiles of four heads of a virtual head
+  int steps;       // MMA steps over q' and over u
+  int smem;        // bytes of a CTA
+};
+TcShape tc_shape(int kk, int kv, int m, int dp, int G);
+cudaError_t tc_launch(const AttnArgs& a, const QParams& kq, const QParams& vq, const TcShape& s, int ctas, cudaStream_t st);
+
+// Codebooks as the tensor-core kernel takes them.
+struct TcBooks {
+  float kalpha[4];      // odd-subset coefficients of the key codebook
+  uint32_t hi[2], lo[2];  // bytes of the 16-bit value levels
+  float unit;           // value of one step of them
+};
 
 }  // namespace paged
 }  // namespace tq

@@ -1,0 +1,506 @@
+// Attention over a paged compressed cache on the 8-bit integer tensor cores,
+// for d_pad 64, 128 and 256 (tq_paged_attn.cuh: the split of the work).
+//
+// A warp is a worker: it takes its share of 32-token block records four at a
+// time (a group), keys and values each staged by bulk copies; the next group's
+// keys load while this one's values are summed, its values while the next keys
+// are scored.  No warp waits for another.
+//
+// Scores.  With the codebook an odd function of its index bits, C[idx] = sum_S
+// alpha_S (2 b_S - 1) over the odd subsets S of the bits (b_S their XOR), the
+// contractions are against 0/1 bits: <q', b_S> per subset and <u, sigma>.  An
+// MMA's A rows are tokens, its K the 32 bits that four threads' words hold at
+// byte distance: `word & (0x01010101 << s)` are four of them with value 2^s,
+// one instruction for four bits.  The B operand carries q' 2^-s in fixed point,
+// 24 bits for s = 0 and 21 for s = 3, as three signed bytes: hi and mid of
+// heads 4 nt .. 4 nt + 3 are tile nt (columns 2 h, 2 h + 1), lo of all of them
+// one more tile (columns 2 h, 2 h + 1: heads h and 4 + h), so that thread
+// column tig holds all of head tig (and 4 + tig).  The queries' images are
+// made once per call (queries_kernel).
+//
+// Values.  The value words of a coordinate (tq_paged_create) turn into 3-bit
+// selectors of eight tokens with two to four bit operations, and byte permutes
+// of a table turn the selectors into the levels' bytes: 16-bit levels, signed
+// hi and unsigned lo byte, four tokens a permute.  Rows are coordinates, K the
+// tokens 4 i + s of the group's four blocks (thread column tig: block tig), B
+// the weights p ||v|| as two bytes (columns 2 h, 2 h + 1) relative to the
+// group's largest.  Products and sums are exact integers; the roundings are
+// those of q', u (2^-21 of the largest entry), the levels and the weights
+// (2^-16 of the largest), and fp32 outside.
+#pragma once
+
+#include "tq_paged_attn.cuh"
+#include "tq_wait.cuh"
+
+namespace tq {
+namespace paged {
+namespace tc {
+
+template <int KK, int KV, int NT, int DP, int MQ>
+struct Shape {
+  static constexpr int WPP = DP / 32, SW = MQ / 32, NK = KK * WPP + SW;
+  static constexpr int GR = NK % 4 == 0 ? 4 : 2;
+  static constexpr int FK = 1 << (KK - 1);  // odd subsets
+  static constexpr int NQ = NT + 1;         // tiles of the scores
+  static constexpr int STEPS = WPP + SW;
+  static constexpr int KB = 32 * NK + 64;        // staged words of a block's keys
+  static constexpr int VB = KV * DP + 32 + 8;    // and values: 8 mod 32, so that four blocks are on different banks
+  static constexpr int WC = 36;                  // words of a column of weights (32 and a gap)
+  static constexpr int WARP_BYTES = 4 * (4 * KB + 4 * VB + 8 * NT * WC) + 16;
+  static constexpr int WARPS = 2;
+  static constexpr int SMEM = WARPS * WARP_BYTES;
+  // resident CTAs: the shared memory's limit, and the registers'
+  static constexpr int BY_SMEM = 233472 / (SMEM + 1024);
+  static constexpr int BY_REGS = DP == 64 ? 8 : DP == 128 ? (NT == 1 ? 6 : 4) : 4;
+  static constexpr int CTAS = BY_SMEM < BY_REGS ? BY_SMEM : BY_REGS;
+  static_assert(NK % 2 == 0 && CTAS >= 1, "shape");
+};
+
+__device__ __forceinline__ uint32_t smem_at(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ void mma_us(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint2 b) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b.x), "r"(b.y));
+}
+__device__ __forceinline__ void mma_su(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint2 b) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.u8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b.x), "r"(b.y));
+}
+__device__ __forceinline__ void mma_uu(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint2 b) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.u8.u8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b.x), "r"(b.y));
+}
+
+__device__ __forceinline__ float pow2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// Place of word base + wt of token 0 in the staged key words, wt in [0, 4); a token is GR words further.
+template <int GR>
+__device__ __forceinline__ int word_place(int base, int wt) {
+  if (GR == 4) return base / 4 * 128 + base % 4 + wt;
+  return (base / 2 + wt / 2) * 64 + wt % 2;
+}
+
+// Products of four bits at a time of a plane word of two tokens with the images from b on.
+template <int N, int NQ>
+__device__ __forceinline__ void score_bits(int (&d)[NQ][4], uint32_t w1, uint32_t w2, const uint2 (*b)[NQ]) {
+  const uint32_t h1 = w1 >> 4, h2 = w2 >> 4;
+#pragma unroll
+  for (int s = 0; s < N; ++s) {
+    const uint32_t k = 0x01010101u << s;
+#pragma unroll
+    for (int t = 0; t < NQ; ++t) mma_us(d[t], w1 & k, w2 & k, h1 & k, h2 & k, b[s][t]);
+  }
+}
+
+// Selectors (nibbles) of the eight tokens 4 i + s from a coordinate's value words.
+template <int KV>
+__device__ __forceinline__ uint32_t selectors(const uint32_t (&w)[KV], int s) {
+  if (KV == 1) return (w[0] >> s) & 0x11111111u;
+  if (KV == 4) return w[s % KV];
+  const uint32_t a = w[(s >> 1) % KV] >> (2 * (s & 1));
+  if (KV == 2) return a & 0x33333333u;
+  const uint32_t b = s < 2 ? w[KV - 1] >> s : __funnelshift_r(w[KV - 1], w[KV - 1], s);
+  return (a & 0x33333333u) | (b & 0x44444444u);
+}
+
+// hi and lo bytes of four tokens' levels; x: their selectors in the low 16 bits
+// (KV = 4: without the signs), neg: theirs as selectors of a byte 0xff.
+template <int KV>
+__device__ __forceinline__ void levels(const TcBooks& K, uint32_t x, uint32_t neg, uint32_t& hi, uint32_t& lo) {
+  hi = __byte_perm(K.hi[0], KV >= 3 ? K.hi[1] : 0u, x);
+  lo = __byte_perm(K.lo[0], KV >= 3 ? K.lo[1] : 0u, x);
+  if constexpr (KV == 4) {
+    const uint32_t s = __byte_perm(0x0000ff00u, 0u, neg);
+    hi ^= s;
+    lo ^= s;
+  }
+}
+
+template <int KK, int KV, int NT, int DP, int MQ>
+__global__ void __launch_bounds__(64, Shape<KK, KV, NT, DP, MQ>::CTAS)
+    attention_tc_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ TcBooks K) {
+  using S = Shape<KK, KV, NT, DP, MQ>;
+  constexpr int WPP = S::WPP, SW = S::SW, NQ = S::NQ, FK = S::FK, STEPS = S::STEPS;
+  extern __shared__ __align__(128) unsigned char smem[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = lane >> 2, tig = lane & 3;
+  uint32_t* kb = reinterpret_cast<uint32_t*>(smem + warp * S::WARP_BYTES);
+  uint32_t* vb = kb + 4 * S::KB;
+  uint32_t* wb = vb + 4 * S::VB;
+  const uint32_t bar_k = smem_at(wb + 8 * NT * S::WC), bar_v = bar_k + 8;
+  if (lane == 0) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar_k));
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar_v));
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncwarp();
+  wait_for_previous();
+  let_next_start();
+
+  const int worker = blockIdx.x * S::WARPS + warp;
+  const int64_t units = A.prefix[A.B] * A.hv, share = share_of(A, units);
+  int64_t u = worker * share;
+  const int64_t u_end = min64(units, u + share);
+  if (u >= u_end) return;
+
+  const uint32_t key_bytes = A.L.o_v * 4u, val_bytes = (A.L.words - A.L.o_v) * 4u;
+  Segment sg = segment_at(A, u, u_end, lane);
+  // lane i < 4 knows of block i of the group at sg.blk: its record (-1: none) and its tokens
+  int64_t at = -1;
+  int nt = 0;
+  auto describe = [&](const Segment& s, int64_t& a, int& n) {
+    a = -1;
+    n = 0;
+    const int blk = s.blk + lane;
+    if (lane < 4 && blk < s.end) {
+      a = record_at(A.L, A.tab, s.b, blk, A.layer, s.h / (A.hv / A.L.hkv));
+      if (a >= 0) n = min(32, s.len - 32 * blk);
+    }
+  };
+  auto stage = [&](int64_t a, bool keys) {
+    const uint32_t there = __ballot_sync(0xffffffffu, a >= 0);
+    const uint32_t bytes = keys ? key_bytes : val_bytes, bar = keys ? bar_k : bar_v;
+    if (lane == 0) expect(bar, __popc(there) * bytes);
+    __syncwarp();
+    if (a >= 0)
+      bulk_copy(smem_at(keys ? kb + lane * S::KB : vb + lane * S::VB), A.pool + a + (keys ? 0 : A.L.o_v), bytes, bar);
+  };
+  describe(sg, at, nt);
+  stage(at, true);
+  stage(at, false);
+
+  // the segment's query images and score constants
+  uint2 bq[STEPS][NQ];
+  float4 cst[NT];
+  auto queries = [&](const Segment& s) {
+    const uint32_t* f = A.frag + ((int64_t)s.b * A.hv + s.h) * A.frag_words;
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i)
+#pragma unroll
+      for (int t = 0; t < NQ; ++t) bq[i][t] = reinterpret_cast<const uint2*>(f)[(i * NQ + t) * 32 + lane];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) cst[t] = reinterpret_cast<const float4*>(f + STEPS * NQ * 64)[4 * t + tig];
+  };
+  queries(sg);
+
+  // thread (g, tig): the tokens 16 h + 4 (r ^ h) + s, r = 0..3, of a block (rows g and g + 8 of two m-tiles;
+  // eight neighbouring tokens modulo 8 per row set, so that their words are on different banks)
+  const int th = g >> 2, ts = g & 3;
+  const uint32_t pack_sel = th ? 0x1504u : 0x5140u;  // bytes lo, lo, hi, hi of two tokens, in the order of i
+  const int wt = WPP == 2 ? tig & 1 : tig, ws = MQ == 64 ? tig & 1 : tig;  // this thread's word of a plane, of the signs
+  const int ksh = WPP == 2 ? 2 * (tig >> 1) : 0, ssh = MQ == 64 ? 2 * (tig >> 1) : 0;
+
+  float m_run[NT], l_run[NT], w_run[NT];
+  float o[NT][DP / 32][4];  // head 4 nt + tig, coordinates 32 c + 4 g + e
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    m_run[n] = -INFINITY;
+    l_run[n] = w_run[n] = 0.f;
+#pragma unroll
+    for (int c = 0; c < DP / 32; ++c) o[n][c][0] = o[n][c][1] = o[n][c][2] = o[n][c][3] = 0.f;
+  }
+
+  bool ok = true;
+  uint32_t phase = 0, k_phase = 0;  // of this group, and of the keys staged last
+  for (;; phase ^= 1u) {
+    // what comes after this group
+    Segment nx = sg;
+    const int step = min(4, sg.end - sg.blk);
+    u += step;
+    nx.blk += step;
+    const bool last = nx.blk == sg.end, done = u >= u_end;
+    if (last && !done) nx = segment_at(A, u, u_end, lane);
+    int64_t nat = -1;
+    int nnt = 0;
+    if (!done) describe(nx, nat, nnt);
+
+    // ---------------- scores, as powers of two
+    if (!(ok = __all_sync(0xffffffffu, bounded_wait<true>(bar_k, phase, A.err)))) break;
+    float x[NT][4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int ni = __shfl_sync(0xffffffffu, nt, i);
+      if (ni == 0) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) x[n][i][0] = x[n][i][1] = x[n][i][2] = x[n][i][3] = -INFINITY;
+        continue;
+      }
+      const uint32_t* kw = kb + i * S::KB;
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const int t1 = 16 * th + 4 * ((2 * m) ^ th) + ts, t2 = 16 * th + 4 * ((2 * m + 1) ^ th) + ts;
+        int acc[FK + 1][NQ][4];
+#pragma unroll
+        for (int f = 0; f <= FK; ++f)
+#pragma unroll
+          for (int t = 0; t < NQ; ++t) acc[f][t][0] = acc[f][t][1] = acc[f][t][2] = acc[f][t][3] = 0;
+        constexpr int KS = WPP == 2 ? 2 : 4, SS = SW == 2 ? 2 : 4;  // steps of a word
+#pragma unroll
+        for (int hf = 0; hf < (WPP + 3) / 4; ++hf) {
+          uint32_t p1[KK], p2[KK];
+#pragma unroll
+          for (int p = 0; p < KK; ++p) {
+            const int base = word_place<S::GR>(p * WPP, wt) + hf * 128;  // hf > 0 only with granules of four
+            p1[p] = kw[base + t1 * S::GR] >> ksh;
+            p2[p] = kw[base + t2 * S::GR] >> ksh;
+          }
+#pragma unroll
+          for (int f = 0; f < FK; ++f) {
+            const uint32_t w1 = f < KK ? p1[f < KK ? f : 0] : p1[0] ^ p1[KK > 1 ? 1 : 0] ^ p1[KK - 1];
+            const uint32_t w2 = f < KK ? p2[f < KK ? f : 0] : p2[0] ^ p2[KK > 1 ? 1 : 0] ^ p2[KK - 1];
+            score_bits<KS, NQ>(acc[f], w1, w2, bq + 4 * hf);
+          }
+        }
+#pragma unroll
+        for (int hf = 0; hf < (SW + 3) / 4; ++hf) {
+          const int base = word_place<S::GR>(KK * WPP, ws) + hf * 128;
+          score_bits<SS, NQ>(acc[FK], kw[base + t1 * S::GR] >> ssh, kw[base + t2 * S::GR] >> ssh, bq + WPP + 4 * hf);
+        }
+        const float n1 = __uint_as_float(kw[32 * S::NK + t1]), n2 = __uint_as_float(kw[32 * S::NK + t2]);
+        const float* rp = reinterpret_cast<const float*>(kw + 32 * S::NK + 32);
+        const float r1 = get_rnorm(rp, t1, A.L.r16), r2 = get_rnorm(rp, t2, A.L.r16);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          // 2^16 hi + 2^8 mid + lo: hi and mid in columns 2 h and 2 h + 1 of tile n, lo in column n of the last
+          auto whole = [&](const int (&d)[NQ][4], int row) {
+            return fmaf(256.f, (float)(256 * d[n][2 * row] + d[n][2 * row + 1]), (float)d[NT][2 * row + n]);
+          };
+          float a1 = 0.f, a2 = 0.f;
+#pragma unroll
+          for (int f = 0; f < FK; ++f) {
+            a1 = fmaf(K.kalpha[f], whole(acc[f], 0), a1);
+            a2 = fmaf(K.kalpha[f], whole(acc[f], 1), a2);
+          }
+          const float y1 = n1 * (fmaf(cst[n].x, a1, cst[n].y) + r1 * fmaf(cst[n].z, whole(acc[FK], 0), cst[n].w));
+          const float y2 = n2 * (fmaf(cst[n].x, a2, cst[n].y) + r2 * fmaf(cst[n].z, whole(acc[FK], 1), cst[n].w));
+          x[n][i][2 * m] = t1 < ni ? y1 : -INFINITY;
+          x[n][i][2 * m + 1] = t2 < ni ? y2 : -INFINITY;
+        }
+      }
+    }
+    __syncwarp();  // the keys have been read
+    if (!done) {
+      stage(nat, true);
+      k_phase ^= 1u;
+    }
+
+    // ---------------- weights
+    if (!(ok = __all_sync(0xffffffffu, bounded_wait<true>(bar_v, phase, A.err)))) break;
+    float corr[NT], back[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float mx = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        mx = fmaxf(mx, fmaxf(fmaxf(x[n][i][0], x[n][i][1]), fmaxf(x[n][i][2], x[n][i][3])));
+#pragma unroll
+      for (int k = 4; k < 32; k *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
+      const float top = fmaxf(m_run[n], mx), base = top == -INFINITY ? 0.f : top;
+      corr[n] = pow2(m_run[n] - base);
+      m_run[n] = top;
+      float l = 0.f, wsum = 0.f, big = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float* vn = reinterpret_cast<const float*>(vb + i * S::VB + KV * DP);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float p = pow2(x[n][i][r] - base);
+          // a slot without a token holds any norm
+          const float w = x[n][i][r] == -INFINITY ? 0.f : p * vn[16 * th + 4 * (r ^ th) + ts];
+          l += p;
+          big = fmaxf(big, w);
+          if (KV == 4) wsum += w;
+          x[n][i][r] = w;
+        }
+      }
+      l_run[n] = fmaf(l_run[n], corr[n], l);
+      if (KV == 4) w_run[n] = fmaf(w_run[n], corr[n], wsum);
+#pragma unroll
+      for (int k = 4; k < 32; k *= 2) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, k));
+      const float inv = big > 1e-33f ? 65535.f / big : 0.f;
+      back[n] = big > 1e-33f ? big * (1.f / 65535.f) * K.unit : 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        // the integer part in the low 16 bits
+        uint32_t b[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) b[r] = __float_as_uint(fmaf(x[n][i][r], inv, 8388608.f));
+        const uint32_t lh0 = __byte_perm(b[0], b[1], pack_sel), lh1 = __byte_perm(b[2], b[3], pack_sel);
+        uint32_t* col = wb + (8 * n + 2 * tig) * S::WC + 8 * i + 2 * ts + th;
+        col[0] = __byte_perm(lh0, lh1, 0x7632);
+        col[S::WC] = __byte_perm(lh0, lh1, 0x5410);
+      }
+    }
+    __syncwarp();
+
+    // ---------------- values
+    uint2 bw[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const uint4* col = reinterpret_cast<const uint4*>(wb + (8 * n + g) * S::WC + 8 * tig);
+      const uint4 a = col[0], b = col[1];
+      bw[n][0] = make_uint2(a.x, a.y);
+      bw[n][1] = make_uint2(a.z, a.w);
+      bw[n][2] = make_uint2(b.x, b.y);
+      bw[n][3] = make_uint2(b.z, b.w);
+    }
+    const uint32_t* vw = vb + tig * S::VB + 4 * g;
+#pragma unroll
+    for (int c = 0; c < DP / 32; ++c) {
+      uint32_t w[4][KV];
+#pragma unroll
+      for (int q = 0; q < KV; ++q) {
+        const uint4 v = *reinterpret_cast<const uint4*>(vw + q * DP + 32 * c);
+        w[0][q] = v.x;
+        w[1][q] = v.y;
+        w[2][q] = v.z;
+        w[3][q] = v.w;
+      }
+      int ah[2][NT][4], al[2][NT][4];  // rows g and g + 8 of m-tile mt: coordinates 2 mt and 2 mt + 1 of the four
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) ah[mt][n][k] = al[mt][n][k] = 0;
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+          uint32_t h[2][2], l[2][2];
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const uint32_t y = selectors<KV>(w[2 * mt + r], s);
+            const uint32_t neg = KV == 4 ? (y >> 3) & 0x11111111u : 0u;
+            const uint32_t z = KV == 4 ? y & 0x77777777u : y;
+            levels<KV>(K, z, neg, h[r][0], l[r][0]);
+            levels<KV>(K, z >> 16, neg >> 16, h[r][1], l[r][1]);
+          }
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            mma_su(ah[mt][n], h[0][0], h[1][0], h[0][1], h[1][1], bw[n][s]);
+            mma_uu(al[mt][n], l[0][0], l[1][0], l[0][1], l[1][1], bw[n][s]);
+          }
+        }
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float hi = (float)(256 * ah[mt][n][2 * r] + ah[mt][n][2 * r + 1]);
+            const float lo = (float)(256 * al[mt][n][2 * r] + al[mt][n][2 * r + 1]);
+            float& t = o[n][c][2 * mt + r];
+            t = fmaf(t, corr[n], back[n] * fmaf(256.f, hi, lo));
+          }
+    }
+    __syncwarp();  // values and weights have been read
+    if (!done) stage(nat, false);
+
+    // ---------------- the segment's part
+    if (last) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        float l = l_run[n], ws = w_run[n];
+#pragma unroll
+        for (int k = 4; k < 32; k *= 2) {
+          l += __shfl_xor_sync(0xffffffffu, l, k);
+          if (KV == 4) ws += __shfl_xor_sync(0xffffffffu, ws, k);
+        }
+        if (4 * n + tig < A.gh) {
+          float* pp = slot_of(A, (int64_t)sg.b * A.hv + sg.h, worker, 4 * n + tig);
+          if (g == 0) *reinterpret_cast<float2*>(pp) = make_float2(m_run[n], l);
+          // four-bit levels stand half a step low (their negatives are complements)
+          const float up = KV == 4 ? 0.5f * K.unit * ws : 0.f;
+#pragma unroll
+          for (int c = 0; c < DP / 32; ++c)
+            *reinterpret_cast<float4*>(pp + 4 + 32 * c + 4 * g) =
+                make_float4(o[n][c][0] + up, o[n][c][1] + up, o[n][c][2] + up, o[n][c][3] + up);
+        }
+        m_run[n] = -INFINITY;
+        l_run[n] = w_run[n] = 0.f;
+#pragma unroll
+        for (int c = 0; c < DP / 32; ++c) o[n][c][0] = o[n][c][1] = o[n][c][2] = o[n][c][3] = 0.f;
+      }
+      if (!done) queries(nx);
+    }
+    if (done) break;
+    sg = nx;
+    at = nat;
+    nt = nnt;
+  }
+  if (!ok) {
+    // a wait ran out (the error word is set): leave empty parts, so that nothing
+    // downstream reads an old workspace, once the copies in flight have landed
+    bounded_wait<true>(bar_k, k_phase, nullptr);
+    bounded_wait<true>(bar_v, phase, nullptr);
+    for (u = worker * share; u < u_end;) {
+      sg = segment_at(A, u, u_end, lane);
+      u += sg.end - sg.blk;
+      if (lane < A.gh)
+        *reinterpret_cast<float2*>(slot_of(A, (int64_t)sg.b * A.hv + sg.h, worker, lane)) = make_float2(-INFINITY, 0.f);
+    }
+  }
+}
+
+// One (d_pad, m, key bits) per source file.
+template <int KK, int KV, int NT, int DP, int MQ>
+cudaError_t launch_one(const AttnArgs& a, const TcBooks& k, int ctas, cudaStream_t st) {
+  using S = Shape<KK, KV, NT, DP, MQ>;
+  auto kern = attention_tc_kernel<KK, KV, NT, DP, MQ>;
+  // function attributes are per device: set on every call (a cheap host call)
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+  if (e != cudaSuccess) return e;
+  return launch_after(kern, dim3(ctas), 32 * S::WARPS, S::SMEM, st, a, k);
+}
+
+template <int KK, int DP, int MQ>
+cudaError_t launch_values(const AttnArgs& a, const TcBooks& k, int kv, int nt, int ctas, cudaStream_t st) {
+  if constexpr (DP == 256) {
+    if (nt != 1) return cudaErrorInvalidValue;
+    switch (kv) {
+      case 1: return launch_one<KK, 1, 1, DP, MQ>(a, k, ctas, st);
+      case 2: return launch_one<KK, 2, 1, DP, MQ>(a, k, ctas, st);
+      case 3: return launch_one<KK, 3, 1, DP, MQ>(a, k, ctas, st);
+      default: return launch_one<KK, 4, 1, DP, MQ>(a, k, ctas, st);
+    }
+  } else {
+    switch (kv * 2 + nt - 1) {
+      case 2: return launch_one<KK, 1, 1, DP, MQ>(a, k, ctas, st);
+      case 3: return launch_one<KK, 1, 2, DP, MQ>(a, k, ctas, st);
+      case 4: return launch_one<KK, 2, 1, DP, MQ>(a, k, ctas, st);
+      case 5: return launch_one<KK, 2, 2, DP, MQ>(a, k, ctas, st);
+      case 6: return launch_one<KK, 3, 1, DP, MQ>(a, k, ctas, st);
+      case 7: return launch_one<KK, 3, 2, DP, MQ>(a, k, ctas, st);
+      case 8: return launch_one<KK, 4, 1, DP, MQ>(a, k, ctas, st);
+      default: return launch_one<KK, 4, 2, DP, MQ>(a, k, ctas, st);
+    }
+  }
+}
+
+// Defined by the source file of its (d_pad, m, key bits).
+template <int KK, int DP, int MQ>
+cudaError_t launch_keys(const AttnArgs& a, const TcBooks& k, int kv, int nt, int ctas, cudaStream_t st);
+
+}  // namespace tc
+}  // namespace paged
+}  // namespace tq

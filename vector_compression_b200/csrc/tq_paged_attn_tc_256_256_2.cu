@@ -1,0 +1,15 @@
+// Tensor-core attention over pages: d_pad 256, m 256, 2-bit key codes.
+#include "tq_paged_attn_tc.cuh"
+
+namespace tq {
+namespace paged {
+namespace tc {
+
+template <>
+cudaError_t launch_keys<2, 256, 256>(const AttnArgs& a, const TcBooks& k, int kv, int nt, int ctas, cudaStream_t st) {
+  return launch_values<2, 256, 256>(a, k, kv, nt, ctas, st);
+}
+
+}  // namespace tc
+}  // namespace paged
+}  // namespace tq
