@@ -18,7 +18,12 @@ inline bool al256(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 255u
 
 // ---------------------------------------------------------------- queries
 
-constexpr float kQMax = 8323072.0f;  // 127 * 2^16: three signed bytes hold it
+// Largest entry in fixed point: the difference of two neighbouring place values,
+// at most 3/2 of it and a rounding, fits three signed bytes (127 2^16 and less).
+constexpr float kQMax = 5548000.0f;
+
+// P_j of the tensor-core kernel's scores: x / 2^j as an integer.
+__device__ __forceinline__ int place_value(float x, int j) { return __float2int_rn(x * (1.f / (float)(1 << j))); }
 
 // Byte `piece` (0: hi, 1: mid, 2: lo) of v = 2^16 hi + 2^8 mid + lo, |v| <= 127 * 2^16, all three in [-128, 127].
 __device__ __forceinline__ uint32_t digit(int v, int piece) {
@@ -125,7 +130,7 @@ __global__ void __launch_bounds__(512) queries_kernel(const AttnArgs A, const QP
       const bool there = slot < A.gh && head < A.G;
       const float* x = which ? us[there ? head : 0] : qs[there ? head : 0];
       const int n = which ? m : dp;
-      const int smask = n == 64 ? 1 : 3;  // coordinate j stands 2^(j & smask) times in the A operand
+      const int in_byte = n == 64 ? 3 : 7;  // coordinate j is bit j & in_byte of its byte (or half byte)
       float mx = 1e-30f, bad = 0.f;
       for (int j = lane; j < n; j += 32) {
         mx = fmaxf(mx, fabsf(x[j]));
@@ -134,11 +139,8 @@ __global__ void __launch_bounds__(512) queries_kernel(const AttnArgs A, const QP
       mx = warp_max(mx);
       bad = warp_sum(bad);
       const float inv = bad == 0.f ? kQMax / mx : 0.f;
-      int sum = 0;  // |sum| < d_pad (127 2^16 + 4) < 2^31
-      for (int j = lane; j < n; j += 32) {
-        const int s = j & smask;
-        sum += __float2int_rn(x[j] * inv * (1.f / (float)(1 << s))) << s;
-      }
+      int sum = 0;  // |sum| < d_pad (kQMax + 2^6) < 2^31
+      for (int j = lane; j < n; j += 32) sum += place_value(x[j] * inv, j & in_byte) << (j & in_byte);
       sum = __reduce_add_sync(0xffffffffu, sum);
       if (lane == 0) {
         if (there) inv_s[which][head] = inv;
@@ -159,13 +161,17 @@ __global__ void __launch_bounds__(512) queries_kernel(const AttnArgs A, const QP
       if (slot < A.gh && head < A.G) {
         const bool which = step >= A32;
         const int n = which ? m : dp, st = which ? step - A32 : step;
-        // bits s + 4 r + 8 i of the thread's word; in two-word planes two threads share one
-        const int s = n == 64 ? st : st & 3;
-        const int j0 = n == 64 ? 32 * (tig & 1) + 2 * (tig >> 1) + s : 32 * (tig + (st & ~3)) + s;
+        // the product of k low bits of the bytes of the thread's word; in two-word planes two threads share one
+        const int k = n == 64 ? 2 * st + 1 + r : (st & 3) + 1 + 4 * r, top = n == 64 ? 4 : 8;
+        const int j0 = n == 64 ? 32 * (tig & 1) + 4 * (tig >> 1) : 32 * (tig + (st & ~3));
         const float* x = which ? us[head] : qs[head];
-        const float k = inv_s[which][head], half = 1.f / (float)(1 << s);
+        const float inv = inv_s[which][head];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w |= digit(__float2int_rn(x[j0 + 4 * r + 8 * i] * k * half), piece) << (8 * i);
+        for (int i = 0; i < 4; ++i) {
+          const float* xi = x + j0 + 8 * i;
+          const int p = place_value(xi[k - 1] * inv, k - 1);
+          w |= digit(k < top ? p - place_value(xi[k] * inv, k) : p, piece) << (8 * i);
+        }
       }
       f0[(int64_t)grp * A.frag_words + (step * NQ + t) * 64 + 2 * ln + r] = w;
     }

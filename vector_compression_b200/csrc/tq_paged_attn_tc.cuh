@@ -9,14 +9,15 @@
 // Scores.  With the codebook an odd function of its index bits, C[idx] = sum_S
 // alpha_S (2 b_S - 1) over the odd subsets S of the bits (b_S their XOR), the
 // contractions are against 0/1 bits: <q', b_S> per subset and <u, sigma>.  An
-// MMA's A rows are tokens, its K the 32 bits that four threads' words hold at
-// byte distance: `word & (0x01010101 << s)` are four of them with value 2^s,
-// one instruction for four bits.  The B operand carries q' 2^-s in fixed point,
-// 24 bits for s = 0 and 21 for s = 3, as three signed bytes: hi and mid of
-// heads 4 nt .. 4 nt + 3 are tile nt (columns 2 h, 2 h + 1), lo of all of them
-// one more tile (columns 2 h, 2 h + 1: heads h and 4 + h), so that thread
-// column tig holds all of head tig (and 4 + tig).  The queries' images are
-// made once per call (queries_kernel).
+// MMA's A rows are tokens, its K four bytes of the word that each of four
+// threads holds: x_k = word & (bytes of k low bits) is one instruction for four
+// of them, k = 1 .. 8 (the whole word), and sum_j b_j q_j = sum_k x_k (P_{k-1} -
+// P_k) with P_j = q_j / 2^j of the byte's bit j (P_8 = 0).  P is in fixed point,
+// an integer, so the differences are exact; three signed bytes hold them: hi
+// and mid of heads 4 nt .. 4 nt + 3 are tile nt (columns 2 h, 2 h + 1), lo of
+// all of them one more tile (columns 2 h, 2 h + 1: heads h and 4 + h), so that
+// thread column tig holds all of head tig (and 4 + tig).  The queries' images
+// are made once per call (queries_kernel).
 //
 // Values.  The value words of a coordinate (tq_paged_create) turn into 3-bit
 // selectors of eight tokens with two to four bit operations, and byte permutes
@@ -25,8 +26,9 @@
 // tokens 4 i + s of the group's four blocks (thread column tig: block tig), B
 // the weights p ||v|| as two bytes (columns 2 h, 2 h + 1) relative to the
 // group's largest.  Products and sums are exact integers; the roundings are
-// those of q', u (2^-21 of the largest entry), the levels and the weights
-// (2^-16 of the largest), and fp32 outside.
+// those of q', u (2^-23 to 2^-16 of the largest entry by the bit's place in its
+// byte, 2^-18 on the average), the levels and the weights (2^-16 of the
+// largest), and fp32 outside.
 #pragma once
 
 #include "tq_paged_attn.cuh"
@@ -99,16 +101,12 @@ __device__ __forceinline__ int word_place(int base, int wt) {
   return (base / 2 + wt / 2) * 64 + wt % 2;
 }
 
-// Products of four bits at a time of a plane word of two tokens with the images from b on.
-template <int N, int NQ>
-__device__ __forceinline__ void score_bits(int (&d)[NQ][4], uint32_t w1, uint32_t w2, const uint2 (*b)[NQ]) {
-  const uint32_t h1 = w1 >> 4, h2 = w2 >> 4;
-#pragma unroll
-  for (int s = 0; s < N; ++s) {
-    const uint32_t k = 0x01010101u << s;
-#pragma unroll
-    for (int t = 0; t < NQ; ++t) mma_us(d[t], w1 & k, w2 & k, h1 & k, h2 & k, b[s][t]);
-  }
+// The low bits of a word's bytes that MMA step `st` takes (x of its first and second half of K): 1 .. 4 and
+// 5 .. 8 bits of whole words, or 1 .. 4 bits of the half of each byte where two threads share a word.
+template <bool SHARED>
+__device__ __forceinline__ constexpr uint32_t low_bits(int st, int second) {
+  const int k = SHARED ? 2 * st + 1 + second : st + 1 + 4 * second;
+  return 0x01010101u * ((1u << k) - 1u);
 }
 
 // Selectors (nibbles) of the eight tokens 4 i + s from a coordinate's value words.
@@ -207,7 +205,7 @@ __global__ void __launch_bounds__(64, Shape<KK, KV, NT, DP, MQ>::CTAS)
   const int th = g >> 2, ts = g & 3;
   const uint32_t pack_sel = th ? 0x1504u : 0x5140u;  // bytes lo, lo, hi, hi of two tokens, in the order of i
   const int wt = WPP == 2 ? tig & 1 : tig, ws = MQ == 64 ? tig & 1 : tig;  // this thread's word of a plane, of the signs
-  const int ksh = WPP == 2 ? 2 * (tig >> 1) : 0, ssh = MQ == 64 ? 2 * (tig >> 1) : 0;
+  const int ksh = WPP == 2 ? 4 * (tig >> 1) : 0, ssh = MQ == 64 ? 4 * (tig >> 1) : 0;
 
   float m_run[NT], l_run[NT], w_run[NT];
   float o[NT][DP / 32][4];  // head 4 nt + tig, coordinates 32 c + 4 g + e
@@ -253,27 +251,40 @@ __global__ void __launch_bounds__(64, Shape<KK, KV, NT, DP, MQ>::CTAS)
         for (int f = 0; f <= FK; ++f)
 #pragma unroll
           for (int t = 0; t < NQ; ++t) acc[f][t][0] = acc[f][t][1] = acc[f][t][2] = acc[f][t][3] = 0;
-        constexpr int KS = WPP == 2 ? 2 : 4, SS = SW == 2 ? 2 : 4;  // steps of a word
+        // the products of a step go to FK + 1 times NQ sums, so that none waits for the one before
+        constexpr int W4 = (WPP + 3) / 4;
 #pragma unroll
-        for (int hf = 0; hf < (WPP + 3) / 4; ++hf) {
-          uint32_t p1[KK], p2[KK];
+        for (int hf = 0; hf < W4; ++hf) {
+          uint32_t w1[FK + 1], w2[FK + 1];
 #pragma unroll
           for (int p = 0; p < KK; ++p) {
             const int base = word_place<S::GR>(p * WPP, wt) + hf * 128;  // hf > 0 only with granules of four
-            p1[p] = kw[base + t1 * S::GR] >> ksh;
-            p2[p] = kw[base + t2 * S::GR] >> ksh;
+            w1[p] = kw[base + t1 * S::GR] >> ksh;
+            w2[p] = kw[base + t2 * S::GR] >> ksh;
+          }
+          if (FK > KK) {
+            w1[FK - 1] = w1[0] ^ w1[1 % KK] ^ w1[KK - 1];
+            w2[FK - 1] = w2[0] ^ w2[1 % KK] ^ w2[KK - 1];
+          }
+          {
+            const int base = word_place<S::GR>(KK * WPP, ws) + hf * 128;
+            w1[FK] = kw[base + t1 * S::GR] >> ssh;
+            w2[FK] = kw[base + t2 * S::GR] >> ssh;
           }
 #pragma unroll
-          for (int f = 0; f < FK; ++f) {
-            const uint32_t w1 = f < KK ? p1[f < KK ? f : 0] : p1[0] ^ p1[KK > 1 ? 1 : 0] ^ p1[KK - 1];
-            const uint32_t w2 = f < KK ? p2[f < KK ? f : 0] : p2[0] ^ p2[KK > 1 ? 1 : 0] ^ p2[KK - 1];
-            score_bits<KS, NQ>(acc[f], w1, w2, bq + 4 * hf);
-          }
-        }
+          for (int st = 0; st < 4; ++st) {
 #pragma unroll
-        for (int hf = 0; hf < (SW + 3) / 4; ++hf) {
-          const int base = word_place<S::GR>(KK * WPP, ws) + hf * 128;
-          score_bits<SS, NQ>(acc[FK], kw[base + t1 * S::GR] >> ssh, kw[base + t2 * S::GR] >> ssh, bq + WPP + 4 * hf);
+            for (int f = 0; f <= FK; ++f) {
+              if (4 * hf + st >= (f < FK ? WPP : SW)) continue;
+              const bool shared_word = f < FK ? WPP == 2 : SW == 2;
+              const uint32_t ka = shared_word ? low_bits<true>(st, 0) : low_bits<false>(st, 0);
+              const uint32_t kb2 = shared_word ? low_bits<true>(st, 1) : low_bits<false>(st, 1);
+              const int step = 4 * hf + st + (f < FK ? 0 : WPP);
+#pragma unroll
+              for (int t = 0; t < NQ; ++t)
+                mma_us(acc[f][t], w1[f] & ka, w2[f] & ka, w1[f] & kb2, w2[f] & kb2, bq[step][t]);
+            }
+          }
         }
         const float n1 = __uint_as_float(kw[32 * S::NK + t1]), n2 = __uint_as_float(kw[32 * S::NK + t2]);
         const float* rp = reinterpret_cast<const float*>(kw + 32 * S::NK + 32);
@@ -292,9 +303,16 @@ __global__ void __launch_bounds__(64, Shape<KK, KV, NT, DP, MQ>::CTAS)
           }
           const float y1 = n1 * (fmaf(cst[n].x, a1, cst[n].y) + r1 * fmaf(cst[n].z, whole(acc[FK], 0), cst[n].w));
           const float y2 = n2 * (fmaf(cst[n].x, a2, cst[n].y) + r2 * fmaf(cst[n].z, whole(acc[FK], 1), cst[n].w));
-          x[n][i][2 * m] = t1 < ni ? y1 : -INFINITY;
-          x[n][i][2 * m + 1] = t2 < ni ? y2 : -INFINITY;
+          x[n][i][2 * m] = y1;
+          x[n][i][2 * m + 1] = y2;
         }
+      }
+      if (ni < 32) {  // slots without a token hold anything
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (16 * th + 4 * (r ^ th) + ts >= ni)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) x[n][i][r] = -INFINITY;
       }
     }
     __syncwarp();  // the keys have been read
@@ -324,8 +342,8 @@ __global__ void __launch_bounds__(64, Shape<KK, KV, NT, DP, MQ>::CTAS)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const float p = pow2(x[n][i][r] - base);
-          // a slot without a token holds any norm
-          const float w = x[n][i][r] == -INFINITY ? 0.f : p * vn[16 * th + 4 * (r ^ th) + ts];
+          // the maximum takes NaN to 0: the norm of a slot without a token can be anything
+          const float w = fmaxf(p * vn[16 * th + 4 * (r ^ th) + ts], 0.f);
           l += p;
           big = fmaxf(big, w);
           if (KV == 4) wsum += w;
