@@ -368,6 +368,9 @@ extern "C" tq_status tq_paged_create(const tq_params* kp, const tq_params* vp, i
   L.o_vn = L.o_v + L.kv * L.dp;
   L.words = L.o_vn + 32;
   L.nb = page / 32;
+  L.nb_shift = -1;
+  for (int i = 0; i < 16; ++i)
+    if (L.nb == 1 << i) L.nb_shift = i;
   L.layers = layers;
   L.hkv = Hkv;
   L.page = page;

@@ -18,6 +18,7 @@ struct Layout {
   int o_kn, o_kr, o_v, o_vn;
   int words;           // of a record
   int nb;              // records of a page per layer and head
+  int nb_shift;        // its logarithm, -1 where it is no power of two
   int layers, hkv, page;
   int64_t page_words;
 };
@@ -34,7 +35,7 @@ struct Table {
 // First word of the record of block `blk` (32 tokens) of a sequence in layer
 // `layer`, head h; -1 in a hole.  64-bit: a pool can be larger than 2^31 words.
 __device__ __forceinline__ int64_t record_at(const Layout& L, const Table& t, int64_t b, int blk, int layer, int h) {
-  const int pi = blk / L.nb;
+  const int pi = L.nb_shift >= 0 ? blk >> L.nb_shift : blk / L.nb;
   const int32_t id = t.rows[b * t.ld + pi];
   if (id < 0 || id >= t.n_pages) return -1;
   return id * L.page_words + ((int64_t)(layer * L.hkv + h) * L.nb + (blk - pi * L.nb)) * L.words;

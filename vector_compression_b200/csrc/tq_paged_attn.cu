@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(128) attention_any_kernel(const AttnArgs A, co
 #pragma unroll
       for (int c = 0; c < NC; ++c) o[g][c] = 0.f;
     for (int blk = sg.blk; blk < sg.end; ++blk) {
-      const int64_t at = record_at(L, A.tab, sg.b, blk, A.layer, sg.h);
+      const int64_t at = record_at(L, A.tab, sg.b, blk, A.layer, sg.kvh);
       if (at < 0) continue;
       const uint32_t* rec = A.pool + at;
       const int nt = min(32, sg.len - 32 * blk);  // tokens of the block

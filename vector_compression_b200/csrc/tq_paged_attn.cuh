@@ -54,6 +54,7 @@ __device__ __forceinline__ int64_t share_of(const AttnArgs& A, int64_t units) {
 
 struct Segment {
   int b, h, blk, end;  // blocks [blk, end) of (sequence, virtual head)
+  int kvh;             // its KV head
   int len;             // tokens of the sequence
 };
 
@@ -74,6 +75,7 @@ __device__ __forceinline__ Segment segment_at(const AttnArgs& A, int64_t u0, int
   Segment s;
   s.b = lo;
   s.h = (int)(rel / nb);
+  s.kvh = s.h / (A.hv / A.L.hkv);
   s.blk = (int)(rel - (int64_t)s.h * nb);
   s.end = (int)min64(nb, s.blk + (u1 - u0));
   s.len = clamp_len(A.lens[lo], A.L, A.tab.max_pages);

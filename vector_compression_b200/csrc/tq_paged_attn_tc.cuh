@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(64, Shape<KK, KV, NT, DP, MQ>::CTAS)
     n = 0;
     const int blk = s.blk + lane;
     if (lane < 4 && blk < s.end) {
-      a = record_at(A.L, A.tab, s.b, blk, A.layer, s.h / (A.hv / A.L.hkv));
+      a = record_at(A.L, A.tab, s.b, blk, A.layer, s.kvh);
       if (a >= 0) n = min(32, s.len - 32 * blk);
     }
   };
@@ -188,7 +188,8 @@ __global__ void __launch_bounds__(64, Shape<KK, KV, NT, DP, MQ>::CTAS)
 
   // the segment's query images and score constants
   uint2 bq[STEPS][NQ];
-  float4 cst[NT];
+  float kc[NT][FK + 1];  // per odd subset, and the constant
+  float2 uc[NT];         // of the signs
   auto queries = [&](const Segment& s) {
     const uint32_t* f = A.frag + ((int64_t)s.b * A.hv + s.h) * A.frag_words;
 #pragma unroll
@@ -196,7 +197,13 @@ __global__ void __launch_bounds__(64, Shape<KK, KV, NT, DP, MQ>::CTAS)
 #pragma unroll
       for (int t = 0; t < NQ; ++t) bq[i][t] = reinterpret_cast<const uint2*>(f)[(i * NQ + t) * 32 + lane];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) cst[t] = reinterpret_cast<const float4*>(f + STEPS * NQ * 64)[4 * t + tig];
+    for (int t = 0; t < NT; ++t) {
+      const float4 c = reinterpret_cast<const float4*>(f + STEPS * NQ * 64)[4 * t + tig];
+#pragma unroll
+      for (int i = 0; i < FK; ++i) kc[t][i] = c.x * K.kalpha[i];
+      kc[t][FK] = c.y;
+      uc[t] = make_float2(c.z, c.w);
+    }
   };
   queries(sg);
 
@@ -291,18 +298,20 @@ __global__ void __launch_bounds__(64, Shape<KK, KV, NT, DP, MQ>::CTAS)
         const float r1 = get_rnorm(rp, t1, A.L.r16), r2 = get_rnorm(rp, t2, A.L.r16);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          // 2^16 hi + 2^8 mid + lo: hi and mid in columns 2 h and 2 h + 1 of tile n, lo in column n of the last
+          // 2^16 hi + 2^8 mid + lo: hi and mid in columns 2 h and 2 h + 1 of tile n, lo in column n of the last.
+          // The whole, a sum of bits times entries, is below 2^31, so that the parts may wrap around.
           auto whole = [&](const int (&d)[NQ][4], int row) {
-            return fmaf(256.f, (float)(256 * d[n][2 * row] + d[n][2 * row + 1]), (float)d[NT][2 * row + n]);
+            return (float)(int)(256u * (256u * (uint32_t)d[n][2 * row] + (uint32_t)d[n][2 * row + 1]) +
+                                (uint32_t)d[NT][2 * row + n]);
           };
-          float a1 = 0.f, a2 = 0.f;
+          float a1 = kc[n][FK], a2 = kc[n][FK];
 #pragma unroll
           for (int f = 0; f < FK; ++f) {
-            a1 = fmaf(K.kalpha[f], whole(acc[f], 0), a1);
-            a2 = fmaf(K.kalpha[f], whole(acc[f], 1), a2);
+            a1 = fmaf(kc[n][f], whole(acc[f], 0), a1);
+            a2 = fmaf(kc[n][f], whole(acc[f], 1), a2);
           }
-          const float y1 = n1 * (fmaf(cst[n].x, a1, cst[n].y) + r1 * fmaf(cst[n].z, whole(acc[FK], 0), cst[n].w));
-          const float y2 = n2 * (fmaf(cst[n].x, a2, cst[n].y) + r2 * fmaf(cst[n].z, whole(acc[FK], 1), cst[n].w));
+          const float y1 = n1 * fmaf(r1, fmaf(uc[n].x, whole(acc[FK], 0), uc[n].y), a1);
+          const float y2 = n2 * fmaf(r2, fmaf(uc[n].x, whole(acc[FK], 1), uc[n].y), a2);
           x[n][i][2 * m] = y1;
           x[n][i][2 * m + 1] = y2;
         }
@@ -323,7 +332,7 @@ __global__ void __launch_bounds__(64, Shape<KK, KV, NT, DP, MQ>::CTAS)
 
     // ---------------- weights
     if (!(ok = __all_sync(0xffffffffu, bounded_wait<true>(bar_v, phase, A.err)))) break;
-    float corr[NT], back[NT];
+    float back[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       float mx = -INFINITY;
@@ -333,7 +342,7 @@ __global__ void __launch_bounds__(64, Shape<KK, KV, NT, DP, MQ>::CTAS)
 #pragma unroll
       for (int k = 4; k < 32; k *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
       const float top = fmaxf(m_run[n], mx), base = top == -INFINITY ? 0.f : top;
-      corr[n] = pow2(m_run[n] - base);
+      const float corr = pow2(m_run[n] - base);
       m_run[n] = top;
       float l = 0.f, wsum = 0.f, big = 0.f;
 #pragma unroll
@@ -350,12 +359,20 @@ __global__ void __launch_bounds__(64, Shape<KK, KV, NT, DP, MQ>::CTAS)
           x[n][i][r] = w;
         }
       }
-      l_run[n] = fmaf(l_run[n], corr[n], l);
-      if (KV == 4) w_run[n] = fmaf(w_run[n], corr[n], wsum);
+      if (__any_sync(0xffffffffu, corr != 1.f)) {  // seldom after a sequence's first groups
+        l_run[n] *= corr;
+        if (KV == 4) w_run[n] *= corr;
+#pragma unroll
+        for (int c = 0; c < DP / 32; ++c)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[n][c][e] *= corr;
+      }
+      l_run[n] += l;
+      if (KV == 4) w_run[n] += wsum;
 #pragma unroll
       for (int k = 4; k < 32; k *= 2) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, k));
       const float inv = big > 1e-33f ? 65535.f / big : 0.f;
-      back[n] = big > 1e-33f ? big * (1.f / 65535.f) * K.unit : 0.f;
+      back[n] = big > 1e-33f ? big * (256.f / 65535.f) * K.unit : 0.f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         // the integer part in the low 16 bits
@@ -425,10 +442,9 @@ __global__ void __launch_bounds__(64, Shape<KK, KV, NT, DP, MQ>::CTAS)
         for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            const float hi = (float)(256 * ah[mt][n][2 * r] + ah[mt][n][2 * r + 1]);
-            const float lo = (float)(256 * al[mt][n][2 * r] + al[mt][n][2 * r + 1]);
-            float& t = o[n][c][2 * mt + r];
-            t = fmaf(t, corr[n], back[n] * fmaf(256.f, hi, lo));
+            // in units of 2^8: what the shift drops is below 2^-8 of a unit, of 2^30 where the weights are large
+            const int v = 256 * ah[mt][n][2 * r] + ah[mt][n][2 * r + 1] + al[mt][n][2 * r] + (al[mt][n][2 * r + 1] >> 8);
+            o[n][c][2 * mt + r] = fmaf(back[n], (float)v, o[n][c][2 * mt + r]);
           }
     }
     __syncwarp();  // values and weights have been read
