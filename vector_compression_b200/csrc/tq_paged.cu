@@ -44,58 +44,73 @@ __device__ __forceinline__ uint32_t transpose32(uint32_t w, int lane) {
   return w;
 }
 
-// The first and last+1 new token (packed numbers) of the sequence that token i
-// belongs to, and its number; false when i belongs to none.
-__device__ __forceinline__ bool find_sequence(const AppendArgs& A, int64_t i, int& b, int64_t& t0, int64_t& t1) {
-  if (!A.cu) {
-    b = (int)i;
-    t0 = i;
-    t1 = i + 1;
-    return true;
-  }
-  if (i < A.cu[0] || i >= A.cu[A.B]) return false;
-  int lo = 0, hi = A.B;  // cu[lo] <= i < cu[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (A.cu[mid] <= i) lo = mid;
-    else hi = mid;
+// The sequence that token i belongs to, and its first and last+1 new token
+// (packed numbers); false when i belongs to none.  Called by a whole warp.
+__device__ __forceinline__ bool find_sequence(const AppendArgs& A, int64_t i, int lane, int& b, int64_t& t0, int64_t& t1) {
+  int lo = 0, n = A.B;  // the last b with cu[b] <= i is in [lo, lo + n)
+  while (n > 1) {
+    const int step = (n + 31) / 32;
+    const uint32_t le = __ballot_sync(0xffffffffu, lane * step < n && A.cu[lo + lane * step] <= i);
+    const int last = le ? 31 - __clz((int)le) : 0;
+    lo += last * step;
+    n = min(step, n - last * step);
   }
   b = lo;
   t0 = A.cu[lo];
-  t1 = A.cu[hi];
-  return t0 <= i && t1 <= A.n_tok;
+  t1 = min64(A.cu[lo + 1], A.n_tok);
+  return t0 <= i && i < t1;
 }
 
-// A warp writes the new tokens that one 32-token block of one head gets (a run).
-// It is started for every token and goes on only for a run's first one.
-__global__ void __launch_bounds__(128) append_kernel(const AppendArgs A) {
-  const Layout& L = A.L;
-  const int lane = threadIdx.x & 31;
-  const int64_t item = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  const int64_t tok = item / L.hkv;
-  const int h = (int)(item - tok * L.hkv);
-  if (tok >= A.n_tok) return;
-  int b;
-  int64_t t0, t1;
-  if (!find_sequence(A, tok, b, t0, t1)) return;
-  const int64_t pos = A.start[b] + (tok - t0);
-  if (pos < 0 || pos >= (int64_t)A.tab.max_pages * L.page) return;
-  const int off = (int)(pos & 31);
-  // the first token at position 0 of a sequence that starts before it begins a run too: 0 mod 32
-  if (tok != t0 && off != 0) return;
-  const int len = (int)min64(32 - off, t1 - tok);
-  const int64_t at = record_at(L, A.tab, b, (int)(pos >> 5), A.layer, h);
-  if (at < 0) return;
-  uint32_t* rec = A.pool + at;
-  const int64_t row0 = tok * L.hkv + h;  // row of token tok + i: row0 + i hkv
-  for (int e = lane; e < len * L.nk; e += 32) {
-    const int i = e / L.nk, w = e - i * L.nk;
-    const int64_t row = row0 + (int64_t)i * L.hkv;
-    rec[key_word_at(L, off + i, w)] = w < L.kw ? A.kcodes[row * L.kw + w] : A.ksigns[row * L.sw + (w - L.kw)];
+// Bits of the plane words p (bit t: token t) that go to value word q.
+template <int KV>
+__device__ __forceinline__ uint32_t place(const uint32_t (&p)[KV], int q) {
+  if (KV == 1) return p[0];
+  constexpr uint32_t m = 0x11111111u;
+  if (KV == 4) {
+    // sign and magnitude: bit 3 below zero, bits 0..2 the distance from the middle
+    const uint32_t n = ~p[3 % KV];
+    return (((p[0] ^ n) >> q) & m) | ((((p[1 % KV] ^ n) >> q) & m) << 1) | ((((p[2 % KV] ^ n) >> q) & m) << 2) |
+           (((n >> q) & m) << 3);
   }
-  const bool mine = lane >= off && lane < off + len;  // lane: place in the block
-  const int64_t row = row0 + (int64_t)(lane - off) * L.hkv;
+  if (q == 2) return __funnelshift_l(p[2 % KV], p[2 % KV], 2);
+  const int s = 2 * q;
+  return ((p[0] >> s) & m) | (((p[1 % KV] >> s) & m) << 1) | (((p[0] >> (s + 1)) & m) << 2) |
+         (((p[1 % KV] >> (s + 1)) & m) << 3);
+}
+
+// A granule of G words from a ROW row to the record.
+template <int G>
+__device__ __forceinline__ void copy_granule(uint32_t* dst, const uint32_t* src) {
+  if (G == 4) *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(src);
+  else if (G == 2) *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(src);
+  else *dst = *src;
+}
+template <int G>
+__device__ __forceinline__ void copy_keys(const AppendArgs& A, uint32_t* rec, int64_t row, int lane) {
+  const Layout& L = A.L;
+  const uint32_t *c = A.kcodes + row * L.kw, *s = A.ksigns + row * L.sw;
+  if (L.kw % G == 0) {
+#pragma unroll 4
+    for (int p = 0; p < L.kw; p += G) copy_granule<G>(rec + (p * 32 + lane * G), c + p);
+#pragma unroll 4
+    for (int p = 0; p < L.sw; p += G) copy_granule<G>(rec + ((L.kw + p) * 32 + lane * G), s + p);
+  } else {
+    for (int w = 0; w < L.nk; ++w) rec[key_word_at(L, lane, w)] = w < L.kw ? c[w] : s[w - L.kw];
+  }
+}
+
+// The new tokens that one 32-token block of one head gets (a run): tok .. tok +
+// len - 1 at places off ...; a lane is a token for the keys and a coordinate of
+// 32 for the values.
+template <int KV>
+__device__ __forceinline__ void write_run(const AppendArgs& A, uint32_t* rec, int h, int64_t tok, int off, int len, int lane) {
+  const Layout& L = A.L;
+  const bool mine = lane >= off && lane < off + len;
+  const int64_t row0 = tok * L.hkv + h, row = row0 + (int64_t)(lane - off) * L.hkv;
   if (mine) {
+    if (L.gr == 4) copy_keys<4>(A, rec, row, lane);
+    else if (L.gr == 2) copy_keys<2>(A, rec, row, lane);
+    else copy_keys<1>(A, rec, row, lane);
     rec[L.o_kn + lane] = __float_as_uint(A.knorms[row]);
     rec[L.o_vn + lane] = __float_as_uint(A.vnorms[row]);
     if (L.r16)
@@ -105,41 +120,70 @@ __global__ void __launch_bounds__(128) append_kernel(const AppendArgs A) {
   }
   const uint32_t own = (len == 32 ? 0xffffffffu : ((1u << len) - 1u)) << off;  // the run's tokens
   const int wpp = L.dp / 32;
-  // bits of the plane words p (bit t: token t) that go to value word q
-  auto place = [&](const uint32_t (&p)[4], int q) -> uint32_t {
-    if (L.kv == 1) return p[0];
-    if (L.kv == 4) {
-      // sign and magnitude: bit 3 below zero, bits 0..2 the distance from the middle
-      const uint32_t n = ~p[3];
-      const uint32_t m = 0x11111111u;
-      return (((p[0] ^ n) >> q) & m) | ((((p[1] ^ n) >> q) & m) << 1) | ((((p[2] ^ n) >> q) & m) << 2) |
-             (((n >> q) & m) << 3);
-    }
-    if (q == 2) return __funnelshift_l(p[2], p[2], 2);
-    const uint32_t m = 0x11111111u;
-    const int s = 2 * q;
-    return ((p[0] >> s) & m) | (((p[1] >> s) & m) << 1) | (((p[0] >> (s + 1)) & m) << 2) | (((p[1] >> (s + 1)) & m) << 3);
-  };
-  for (int jw = 0; jw < wpp; ++jw) {
-    uint32_t p[4] = {0u, 0u, 0u, 0u};
+  // the bits of the run's fields: the same placement of codes of ones
+  uint32_t ones[KV];
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      if (q < L.kv) p[q] = transpose32(mine ? A.vcodes[row * (L.kv * wpp) + q * wpp + jw] : 0u, lane);
-    for (int q = 0; q < L.kv; ++q) {
-      uint32_t* w = rec + L.o_v + q * L.dp + 32 * jw + lane;
-      // the mask of the run's fields: the same placement of a code of ones
-      // (for k = 4 of the fields' four bits)
-      uint32_t f[4] = {own, own, own, own};
-      uint32_t msk;
-      if (L.kv == 4) {
-        const uint32_t m = (own >> q) & 0x11111111u;
-        msk = m * 15u;
-      } else {
-        msk = place(f, q);
-      }
-      const uint32_t v = place(p, q) & msk;
-      *w = own == 0xffffffffu ? v : ((*w & ~msk) | v);
+  for (int q = 0; q < KV; ++q) ones[q] = own;
+#pragma unroll 4
+  for (int jw = 0; jw < wpp; ++jw) {
+    uint32_t* w = rec + L.o_v + 32 * jw + lane;
+    uint32_t old[KV], p[KV];
+    if (own != 0xffffffffu) {
+#pragma unroll
+      for (int q = 0; q < KV; ++q) old[q] = w[q * L.dp];
     }
+    if (len <= 4) {  // below that many tokens picking their bits is shorter than the transposition of 32
+#pragma unroll
+      for (int q = 0; q < KV; ++q) p[q] = 0;
+      for (int i = 0; i < len; ++i) {
+#pragma unroll
+        for (int q = 0; q < KV; ++q)
+          p[q] |= ((A.vcodes[(row0 + (int64_t)i * L.hkv) * (KV * wpp) + q * wpp + jw] >> lane) & 1u) << (off + i);
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < KV; ++q) p[q] = transpose32(mine ? A.vcodes[row * (KV * wpp) + q * wpp + jw] : 0u, lane);
+    }
+#pragma unroll
+    for (int q = 0; q < KV; ++q) {
+      // of four-bit codes a field's four bits lie in one word
+      const uint32_t msk = KV == 4 ? ((own >> q) & 0x11111111u) * 15u : place<KV>(ones, q);
+      const uint32_t v = place<KV>(p, q) & msk;
+      w[q * L.dp] = own == 0xffffffffu ? v : ((old[q] & ~msk) | v);
+    }
+  }
+}
+
+// Tokens that a warp looks through for the first ones of runs: the 32 of a
+// prompt's block then cost four warps' look, and a step's single tokens (cu ==
+// null, a token per warp) wait for no other.
+constexpr int kAppendTile = 8;
+
+template <int KV>
+__global__ void __launch_bounds__(128) append_kernel(const AppendArgs A) {
+  const Layout& L = A.L;
+  const int lane = threadIdx.x & 31;
+  const int64_t item = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  const int64_t tile = item / L.hkv;
+  const int h = (int)(item - tile * L.hkv);
+  const int per = A.cu ? kAppendTile : 1;
+  const int64_t end = min64(A.n_tok, (tile + 1) * per);
+  for (int64_t tok = tile * per; tok < end;) {
+    int b = (int)tok;
+    int64_t t0 = tok, t1 = tok + 1;
+    if (A.cu && !find_sequence(A, tok, lane, b, t0, t1)) {
+      ++tok;
+      continue;
+    }
+    const int64_t pos = A.start[b] + (tok - t0);
+    const int off = (int)(pos & 31);
+    const int len = (int)min64(32 - off, t1 - tok);
+    // a sequence's first new token begins a run, and so does every block's first
+    if ((tok == t0 || off == 0) && pos >= 0 && pos < (int64_t)A.tab.max_pages * L.page) {
+      const int64_t at = record_at(L, A.tab, b, (int)(pos >> 5), A.layer, h);
+      if (at >= 0) write_run<KV>(A, A.pool + at, h, tok, off, len, lane);
+    }
+    tok += len;
   }
 }
 
@@ -409,9 +453,15 @@ extern "C" tq_status tq_paged_append(const tq_paged* pg, uint32_t* pool, int64_t
     return TQ_ERR_INVALID_ARG;
   AppendArgs a = {L, {tables, table_ld, max_pages, n_pages}, pool, layer, kcodes, ksigns, vcodes, knorms, krnorms,
                   vnorms, n_tok, B, cu, start};
-  const int64_t blocks = tq::ceil_div(n_tok * L.hkv, 4);
+  const int64_t blocks = tq::ceil_div(tq::ceil_div(n_tok, cu ? kAppendTile : 1) * L.hkv, 4);
   if (blocks > 0x7fffffffll) return TQ_ERR_UNSUPPORTED;
-  append_kernel<<<(unsigned)blocks, 128, 0, static_cast<cudaStream_t>(stream)>>>(a);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  switch (L.kv) {
+    case 1: append_kernel<1><<<(unsigned)blocks, 128, 0, st>>>(a); break;
+    case 2: append_kernel<2><<<(unsigned)blocks, 128, 0, st>>>(a); break;
+    case 3: append_kernel<3><<<(unsigned)blocks, 128, 0, st>>>(a); break;
+    default: append_kernel<4><<<(unsigned)blocks, 128, 0, st>>>(a); break;
+  }
   return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
 }
 

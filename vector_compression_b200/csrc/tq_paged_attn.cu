@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(512) queries_kernel(const AttnArgs A, const QP
   const int m = kq.m;
   if (h == 0) {
     long long sum = 0;
-    for (int i = tid; i < b; i += 512) sum += (clamp_len(A.lens[i], A.L, A.tab.max_pages) + 31) / 32;
+    for (int i = tid; i < b; i += 512) sum += blocks_of(A, i);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane == 0) s_sum[warp] = sum;
@@ -83,14 +83,14 @@ __global__ void __launch_bounds__(512) queries_kernel(const AttnArgs A, const QP
     long long sum = 0;
     for (int i = 0; i < 16; ++i) sum += s_sum[i];
     A.prefix[b] = sum;
-    if (b == A.B - 1) A.prefix[A.B] = sum + (clamp_len(A.lens[b], A.L, A.tab.max_pages) + 31) / 32;
+    if (b == A.B - 1) A.prefix[A.B] = sum + blocks_of(A, b);
   }
   const int parts = m < 512 ? 512 / m : 1, len = (dp + parts - 1) / parts;  // of the coordinates
   for (int g0 = 0; g0 < A.G; g0 += 4) {
     for (int e = tid; e < m * parts; e += 512) {
       const int i = e % m, j0 = e / m * len, j1 = min(dp, j0 + len);
       float acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 16
+#pragma unroll 32
       for (int j = j0; j < j1; ++j) {
         const float s = kq.St[(int64_t)j * m + i];
 #pragma unroll
@@ -327,12 +327,14 @@ __global__ void __launch_bounds__(128) attention_any_kernel(const AttnArgs A, co
 
 // ---------------------------------------------------------------- join
 
-// Block (b, query head), four warps: the parts' maximum, then warp w sums parts
-// w, w + 4, ... and warp 0 adds the four sums, rotates back and stores.
+constexpr int kJoinWarps = 8;
+
+// Block (b, query head): the parts' maximum, then warp w sums parts w, w + 8,
+// ... and warp 0 adds the warps' sums, rotates back and stores.
 template <int A32>
-__global__ void __launch_bounds__(128) join_kernel(const AttnArgs A, const QParams vq) {
+__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const AttnArgs A, const QParams vq) {
   constexpr int dp = 32 * A32;
-  __shared__ float sm[4], sl[4], sv[4][dp];
+  __shared__ float sm[kJoinWarps], sl[kJoinWarps], sv[kJoinWarps][dp];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.x / A.Hq, hq = blockIdx.x % A.Hq;
   const int kh = hq / A.G, gq = hq % A.G;
@@ -345,16 +347,17 @@ __global__ void __launch_bounds__(128) join_kernel(const AttnArgs A, const QPara
   // parts c0 .. c1; none of an empty sequence
   const int c0 = (int)(s0 / share), c1 = n ? (int)((s0 + n - 1) / share) : c0 - 1;
   float top = -INFINITY;
-  for (int c = c0 + tid; c <= c1; c += 128) top = fmaxf(top, slot_of(A, bh, c, g)[0]);
+  for (int c = c0 + tid; c <= c1; c += 32 * kJoinWarps) top = fmaxf(top, slot_of(A, bh, c, g)[0]);
   top = warp_max(top);
   if (lane == 0) sm[warp] = top;
   __syncthreads();
-  top = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, sm[w]);
   float l = 0.f, v[A32];
 #pragma unroll
   for (int a = 0; a < A32; ++a) v[a] = 0.f;
-#pragma unroll 2
-  for (int c = c0 + warp; c <= c1; c += 4) {
+#pragma unroll 4
+  for (int c = c0 + warp; c <= c1; c += kJoinWarps) {
     const float* pp = slot_of(A, bh, c, g);
     const float pl = pp[1];
     // holes only: nothing in it (a NaN sum is not zero: it goes on)
@@ -368,10 +371,15 @@ __global__ void __launch_bounds__(128) join_kernel(const AttnArgs A, const QPara
   for (int a = 0; a < A32; ++a) sv[warp][32 * a + lane] = v[a];
   __syncthreads();
   if (warp != 0) return;
-  l = sl[0] + sl[1] + sl[2] + sl[3];
+  l = 0.f;
 #pragma unroll
-  for (int a = 0; a < A32; ++a)
-    v[a] = sv[0][32 * a + lane] + sv[1][32 * a + lane] + sv[2][32 * a + lane] + sv[3][32 * a + lane];
+  for (int a = 0; a < A32; ++a) v[a] = 0.f;
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) {
+    l += sl[w];
+#pragma unroll
+    for (int a = 0; a < A32; ++a) v[a] += sv[w][32 * a + lane];
+  }
   // no token: zeros; (a NaN sum is not zero and stays one)
   const float inv = l == 0.f ? 0.f : vq.inv_sqrt_dpad / l;
   warp_fwht<A32>(v, lane);
@@ -440,7 +448,7 @@ cudaError_t run(const AttnArgs& a, const tq_paged* pg, const Plan& p, cudaStream
     if (e == cudaSuccess) e = launch_after(attention_any_kernel<NC>, dim3(a.workers), 128, smem, st, a, pg->kq, pg->vq);
   }
   if (e != cudaSuccess) return e;
-  e = launch_after(join_kernel<A32>, dim3((unsigned)(a.B * a.Hq)), 128, 0, st, a, pg->vq);
+  e = launch_after(join_kernel<A32>, dim3((unsigned)(a.B * a.Hq)), 32 * kJoinWarps, 0, st, a, pg->vq);
   const cudaError_t last = cudaGetLastError();
   return e != cudaSuccess ? e : last;
 }

@@ -52,13 +52,29 @@ __device__ __forceinline__ int64_t share_of(const AttnArgs& A, int64_t units) {
   return s < kMinShare ? kMinShare : s;
 }
 
+__device__ __forceinline__ int blocks_of(const AttnArgs& A, int64_t b) {
+  return (clamp_len(A.lens[b], A.L, A.tab.max_pages) + 31) / 32;
+}
+
 struct Segment {
   int b, h, blk, end;  // blocks [blk, end) of (sequence, virtual head)
   int kvh;             // its KV head
   int len;             // tokens of the sequence
 };
 
-// The segment that unit u0 begins, cut at u1; called by a whole warp.
+// The segment that begins n_units before the share's end at unit `rel` of sequence b, which has nb blocks a head.
+__device__ __forceinline__ Segment segment_in(const AttnArgs& A, int b, int nb, int64_t rel, int64_t n_units) {
+  Segment s;
+  s.b = b;
+  s.h = (int)(rel / nb);
+  s.kvh = s.h / (A.hv / A.L.hkv);
+  s.blk = (int)(rel - (int64_t)s.h * nb);
+  s.end = (int)min64(nb, s.blk + n_units);
+  s.len = clamp_len(A.lens[b], A.L, A.tab.max_pages);
+  return s;
+}
+
+// The segment that unit u0 begins, cut at u1, found in the blocks' prefix sums; called by a whole warp.
 __device__ __forceinline__ Segment segment_at(const AttnArgs& A, int64_t u0, int64_t u1, int lane) {
   const int64_t x = u0 / A.hv;
   int lo = 0, n = A.B;  // the last b with prefix[b] <= x is in [lo, lo + n)
@@ -70,16 +86,51 @@ __device__ __forceinline__ Segment segment_at(const AttnArgs& A, int64_t u0, int
     n = min(step, n - last * step);
   }
   const int64_t p = A.prefix[lo];
-  const int nb = (int)(A.prefix[lo + 1] - p);
-  const int64_t rel = u0 - A.hv * p;
-  Segment s;
-  s.b = lo;
-  s.h = (int)(rel / nb);
-  s.kvh = s.h / (A.hv / A.L.hkv);
-  s.blk = (int)(rel - (int64_t)s.h * nb);
-  s.end = (int)min64(nb, s.blk + (u1 - u0));
-  s.len = clamp_len(A.lens[lo], A.L, A.tab.max_pages);
-  return s;
+  return segment_in(A, lo, (int)(A.prefix[lo + 1] - p), u0 - A.hv * p, u1 - u0);
+}
+
+// The segment behind s, for a share that goes on to u1; u0 is its first unit.
+__device__ __forceinline__ Segment segment_after(const AttnArgs& A, const Segment& s, int64_t u0, int64_t u1) {
+  int b = s.b, nb = blocks_of(A, b);
+  int64_t rel = (int64_t)(s.h + 1) * nb;
+  if (s.h + 1 == A.hv) {
+    rel = 0;
+    do nb = blocks_of(A, ++b);
+    while (nb == 0);  // ends: a unit u0 < u1 <= units is some sequence's
+  }
+  return segment_in(A, b, nb, rel, u1 - u0);
+}
+
+// Up to this many sequences a warp sums their blocks itself, and need not wait for the prefix sums.
+constexpr int kOwnSums = 1024;
+
+// A worker's first segment and its share [u0, u1) of the units from the lengths alone; B <= kOwnSums, a whole warp.
+__device__ __forceinline__ Segment first_segment(const AttnArgs& A, int worker, int64_t& u0, int64_t& u1, int lane) {
+  const int per = (A.B + 31) / 32, b0 = lane * per, b1 = min(A.B, b0 + per);
+  long long mine = 0;
+  for (int b = b0; b < b1; ++b) mine += blocks_of(A, b);
+  long long upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += x;
+  }
+  const int64_t units = __shfl_sync(0xffffffffu, upto, 31) * A.hv, share = share_of(A, units);
+  u0 = worker * share;
+  u1 = min64(units, u0 + share);
+  Segment s = {};
+  if (u0 >= u1) return s;
+  const long long x = u0 / A.hv, before = upto - mine;
+  // the last lane whose sequences begin at or before x (it has blocks: the next lane's begin behind x)
+  const int at = __popc(__ballot_sync(0xffffffffu, before <= x)) - 1;
+  int b = at * per, nb = 0;
+  long long p = __shfl_sync(0xffffffffu, before, at);
+  for (;; ++b) {
+    nb = blocks_of(A, b);
+    if (p + nb > x) break;
+    p += nb;
+  }
+  return segment_in(A, b, nb, u0 - A.hv * p, u1 - u0);
 }
 
 __host__ __device__ __forceinline__ int part_row(int dp) { return dp + 4; }  // 16-byte rows

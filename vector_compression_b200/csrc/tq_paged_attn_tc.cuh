@@ -151,17 +151,29 @@ __global__ void __launch_bounds__(64, Shape<KK, KV, NT, DP, MQ>::CTAS)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   __syncwarp();
-  wait_for_previous();
   let_next_start();
 
+  // the first records are on their way before the queries are ready
   const int worker = blockIdx.x * S::WARPS + warp;
-  const int64_t units = A.prefix[A.B] * A.hv, share = share_of(A, units);
-  int64_t u = worker * share;
-  const int64_t u_end = min64(units, u + share);
-  if (u >= u_end) return;
+  const bool own_sums = A.B <= kOwnSums;
+  int64_t u, u_end;
+  Segment sg;
+  if (own_sums) {
+    sg = first_segment(A, worker, u, u_end, lane);
+  } else {
+    wait_for_previous();
+    const int64_t units = A.prefix[A.B] * A.hv, share = share_of(A, units);
+    u = worker * share;
+    u_end = min64(units, u + share);
+    if (u < u_end) sg = segment_at(A, u, u_end, lane);
+  }
+  const int64_t u_first = u;
+  if (u >= u_end) {
+    if (own_sums) wait_for_previous();  // the join's launch counts on this one being behind the queries
+    return;
+  }
 
   const uint32_t key_bytes = A.L.o_v * 4u, val_bytes = (A.L.words - A.L.o_v) * 4u;
-  Segment sg = segment_at(A, u, u_end, lane);
   // lane i < 4 knows of block i of the group at sg.blk: its record (-1: none) and its tokens
   int64_t at = -1;
   int nt = 0;
@@ -205,6 +217,7 @@ __global__ void __launch_bounds__(64, Shape<KK, KV, NT, DP, MQ>::CTAS)
       uc[t] = make_float2(c.z, c.w);
     }
   };
+  if (own_sums) wait_for_previous();
   queries(sg);
 
   // thread (g, tig): the tokens 16 h + 4 (r ^ h) + s, r = 0..3, of a block (rows g and g + 8 of two m-tiles;
@@ -233,7 +246,7 @@ __global__ void __launch_bounds__(64, Shape<KK, KV, NT, DP, MQ>::CTAS)
     u += step;
     nx.blk += step;
     const bool last = nx.blk == sg.end, done = u >= u_end;
-    if (last && !done) nx = segment_at(A, u, u_end, lane);
+    if (last && !done) nx = segment_after(A, sg, u, u_end);
     int64_t nat = -1;
     int nnt = 0;
     if (!done) describe(nx, nat, nnt);
@@ -487,7 +500,7 @@ __global__ void __launch_bounds__(64, Shape<KK, KV, NT, DP, MQ>::CTAS)
     // downstream reads an old workspace, once the copies in flight have landed
     bounded_wait<true>(bar_k, k_phase, nullptr);
     bounded_wait<true>(bar_v, phase, nullptr);
-    for (u = worker * share; u < u_end;) {
+    for (u = u_first; u < u_end;) {
       sg = segment_at(A, u, u_end, lane);
       u += sg.end - sg.blk;
       if (lane < A.gh)

@@ -14,6 +14,7 @@
 // sines and cosines of a token serve all of a group's heads.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <new>
@@ -44,7 +45,7 @@ struct Args {
   int64_t items;  // (token, block of heads)
   int d, rot, blocks, hpg;  // blocks of hpg heads per token
   int lanes;      // of a group: a power of two
-  float eps, mscale;
+  float eps, mscale, inv_d;
   uint64_t turn[128];
 };
 
@@ -76,16 +77,17 @@ __device__ __forceinline__ void store(T* p, const float (&v)[V]) {
   *reinterpret_cast<Vec<T, V>*>(p) = r;
 }
 
-// A chunk is what one lane handles at a time: V pairs (two vectors, at `a` and
-// `b` of the row) or, behind the rotated part, V coordinates that pass (`a`).
+// A chunk is what one lane handles at a time, two vectors at `a` and `b` of the
+// row: V pairs, or, behind the rotated part, 2 V coordinates that pass (the
+// last of them perhaps V: b = -1).
 template <int V, bool PAIRS>
-__device__ __forceinline__ void chunk_at(int c, int np, int rot, int& a, int& b) {
+__device__ __forceinline__ void chunk_at(int c, int np, const Args& A, int& a, int& b) {
   if (c < np) {
     a = PAIRS ? 2 * V * c : V * c;
-    b = PAIRS ? a + V : a + rot / 2;
+    b = PAIRS ? a + V : a + A.rot / 2;
   } else {
-    a = rot + V * (c - np);
-    b = -1;
+    a = A.rot + 2 * V * (c - np);
+    b = a + V < A.d ? a + V : -1;
   }
 }
 
@@ -126,6 +128,61 @@ __device__ __forceinline__ void rotate(float (&x)[V], float (&z)[V], const float
   }
 }
 
+// Rows of one side: V pairs (or coordinates that pass) a lane, U heads' loads in flight.
+template <typename T, int V, bool PAIRS, int U>
+__device__ __forceinline__ void norm_rope_rows(const Args& A, const Side& s, int64_t tok, int h0, int h1, int lane,
+                                               unsigned mask, bool there, bool turn, int a, int b, const float (&co)[V],
+                                               const float (&si)[V]) {
+  const T* x = static_cast<const T*>(s.x) + tok * s.xt + a;
+  T* y = static_cast<T*>(s.y) + tok * s.yt + a;
+  const int ab = b - a;
+  float g0[V], g1[V];
+  if (s.w && there) {
+    load<T, V>(static_cast<const T*>(s.w) + a, g0);
+    if (b >= 0) load<T, V>(static_cast<const T*>(s.w) + b, g1);
+  }
+  for (int h = h0; h < h1; h += U) {
+    Vec<T, V> r0[U], r1[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (there && h + u < h1) {
+        r0[u] = *reinterpret_cast<const Vec<T, V>*>(x + (h + u) * s.xh);
+        if (b >= 0) r1[u] = *reinterpret_cast<const Vec<T, V>*>(x + (h + u) * s.xh + ab);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (h + u >= h1) break;
+      float p[V], q[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        p[i] = there ? to_f32(r0[u].e[i]) : 0.f;
+        q[i] = there && b >= 0 ? to_f32(r1[u].e[i]) : 0.f;
+      }
+      if (s.w) {
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) sum = fmaf(p[i], p[i], fmaf(q[i], q[i], sum));
+        for (int o = A.lanes >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(mask, sum, o);
+        const float inv = rsqrtf(sum * A.inv_d + A.eps);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          p[i] *= inv * g0[i];
+          q[i] *= inv * g1[i];
+        }
+      }
+      if (!there) continue;
+      if (b >= 0) {
+        if (turn) rotate<V, PAIRS>(p, q, co, si);
+        store<T, V>(y + (h + u) * s.yh + ab, q);
+      }
+      store<T, V>(y + (h + u) * s.yh, p);
+    }
+  }
+}
+
+// A group of lanes takes hpg heads of a token, a chunk of the row per lane: the
+// row is read once, and the sines serve all of the heads.
 template <typename T, int V, bool PAIRS>
 __global__ void __launch_bounds__(256) norm_rope_kernel(const __grid_constant__ Args A) {
   const int lane = threadIdx.x & (A.lanes - 1);
@@ -133,69 +190,90 @@ __global__ void __launch_bounds__(256) norm_rope_kernel(const __grid_constant__ 
   const int64_t item = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / A.lanes;
   if (item >= A.items) return;
   const int64_t tok = item / A.blocks;
-  const int h0 = (int)(item - tok * A.blocks) * A.hpg;
-  const int h1 = min(h0 + A.hpg, A.s[0].heads + A.s[1].heads);
-  const int np = A.rot / 2 / V, nc = np + (A.d - A.rot) / V;
+  const int h0 = (int)(item - tok * A.blocks) * A.hpg, hq = A.s[0].heads;
+  const int h1 = min(h0 + A.hpg, hq + A.s[1].heads);
+  const int np = A.rot / 2 / V, nc = np + (A.d - A.rot + 2 * V - 1) / (2 * V);
+  const bool there = lane < nc, turn = lane < np;
+  int a = 0, b = -1;
+  if (there) chunk_at<V, PAIRS>(lane, np, A, a, b);
+  float co[V] = {}, si[V] = {};
+  if (turn) turns<V>(A, lane, (uint64_t)A.pos[tok], co, si);
+  constexpr int U = V > 1 ? 4 : 2;
+  if (h0 < hq) norm_rope_rows<T, V, PAIRS, U>(A, A.s[0], tok, h0, min(h1, hq), lane, mask, there, turn, a, b, co, si);
+  if (h1 > hq) norm_rope_rows<T, V, PAIRS, U>(A, A.s[1], tok, max(h0, hq) - hq, h1 - hq, lane, mask, there, turn, a, b, co, si);
+}
+
+// Rows of more than 32 chunks (long heads, or no alignment for vectors): a warp per (token, head), chunk by chunk.
+template <typename T, int V, bool PAIRS>
+__global__ void __launch_bounds__(256) norm_rope_wide_kernel(const __grid_constant__ Args A) {
+  const int lane = threadIdx.x & 31;
+  const int64_t item = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  if (item >= A.items) return;
+  const int64_t tok = item / A.blocks;
+  const int h = (int)(item - tok * A.blocks);
+  const bool isk = h >= A.s[0].heads;
+  const Side& s = A.s[isk ? 1 : 0];
+  const int hh = isk ? h - A.s[0].heads : h;
+  const int np = A.rot / 2 / V, nc = np + (A.d - A.rot + 2 * V - 1) / (2 * V);
   const uint64_t pos = A.rot ? (uint64_t)A.pos[tok] : 0;
-  for (int h = h0; h < h1; ++h) {
-    const bool isk = h >= A.s[0].heads;
-    const Side& s = A.s[isk ? 1 : 0];
-    const int hh = isk ? h - A.s[0].heads : h;
-    const T* x = static_cast<const T*>(s.x) + tok * s.xt + hh * s.xh;
-    T* y = static_cast<T*>(s.y) + tok * s.yt + hh * s.yh;
-    const T* w = static_cast<const T*>(s.w);
-    float inv = 1.f;
-    if (w) {
-      float sum = 0.f;
-      for (int c = lane; c < nc; c += A.lanes) {
-        int a, b;
-        chunk_at<V, PAIRS>(c, np, A.rot, a, b);
-        float u[V];
-        load<T, V>(x + a, u);
+  const T* x = static_cast<const T*>(s.x) + tok * s.xt + hh * s.xh;
+  T* y = static_cast<T*>(s.y) + tok * s.yt + hh * s.yh;
+  const T* w = static_cast<const T*>(s.w);
+  float inv = 1.f;
+  if (w) {
+    float sum = 0.f;
+    for (int c = lane; c < nc; c += 32) {
+      int a, b;
+      chunk_at<V, PAIRS>(c, np, A, a, b);
+      float u[V];
+      load<T, V>(x + a, u);
+#pragma unroll
+      for (int i = 0; i < V; ++i) sum = fmaf(u[i], u[i], sum);
+      if (b >= 0) {
+        load<T, V>(x + b, u);
 #pragma unroll
         for (int i = 0; i < V; ++i) sum = fmaf(u[i], u[i], sum);
-        if (b >= 0) {
-          load<T, V>(x + b, u);
-#pragma unroll
-          for (int i = 0; i < V; ++i) sum = fmaf(u[i], u[i], sum);
-        }
       }
-      for (int o = A.lanes >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(mask, sum, o);
-      inv = rsqrtf(sum / (float)A.d + A.eps);
     }
-    for (int c = lane; c < nc; c += A.lanes) {
-      int a, b;
-      chunk_at<V, PAIRS>(c, np, A.rot, a, b);
-      float u[V], v[V], g[V];
-      load<T, V>(x + a, u);
+    inv = rsqrtf(warp_sum(sum) * A.inv_d + A.eps);
+  }
+  for (int c = lane; c < nc; c += 32) {
+    int a, b;
+    chunk_at<V, PAIRS>(c, np, A, a, b);
+    float u[V], v[V], g[V];
+    load<T, V>(x + a, u);
+    if (w) {
+      load<T, V>(w + a, g);
+#pragma unroll
+      for (int i = 0; i < V; ++i) u[i] = u[i] * inv * g[i];
+    }
+    if (b >= 0) {
+      load<T, V>(x + b, v);
       if (w) {
-        load<T, V>(w + a, g);
+        load<T, V>(w + b, g);
 #pragma unroll
-        for (int i = 0; i < V; ++i) u[i] = u[i] * inv * g[i];
+        for (int i = 0; i < V; ++i) v[i] = v[i] * inv * g[i];
       }
-      if (b >= 0) {
-        load<T, V>(x + b, v);
-        if (w) {
-          load<T, V>(w + b, g);
-#pragma unroll
-          for (int i = 0; i < V; ++i) v[i] = v[i] * inv * g[i];
-        }
+      if (c < np) {
         float co[V], si[V];
         turns<V>(A, c, pos, co, si);
         rotate<V, PAIRS>(u, v, co, si);
-        store<T, V>(y + b, v);
       }
-      store<T, V>(y + a, u);
+      store<T, V>(y + b, v);
     }
+    store<T, V>(y + a, u);
   }
 }
 
 template <typename T, int V>
-int launch(const Args& a, bool pairs, cudaStream_t st) {
+int launch(const Args& a, bool pairs, bool wide, cudaStream_t st) {
   const int64_t blocks = ceil_div(a.items * a.lanes, 256);
   if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
-  if (pairs) norm_rope_kernel<T, V, true><<<(unsigned)blocks, 256, 0, st>>>(a);
-  else norm_rope_kernel<T, V, false><<<(unsigned)blocks, 256, 0, st>>>(a);
+  const unsigned n = (unsigned)blocks;
+  if (wide && pairs) norm_rope_wide_kernel<T, V, true><<<n, 256, 0, st>>>(a);
+  else if (wide) norm_rope_wide_kernel<T, V, false><<<n, 256, 0, st>>>(a);
+  else if (pairs) norm_rope_kernel<T, V, true><<<n, 256, 0, st>>>(a);
+  else norm_rope_kernel<T, V, false><<<n, 256, 0, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -289,19 +367,25 @@ extern "C" tq_status tq_qk_norm_rope(const tq_rope* rope, tq_dtype dt, int64_t n
   const bool pairs = rope && rope->interleaved;
   int v = dt == TQ_F32 ? 4 : 8;
   while (v > 1 && !fits(a, pairs, esz, v)) v = v == 8 ? 4 : 1;
-  const int chunks = a.rot / 2 / v + (d - a.rot) / v;
+  a.inv_d = 1.0f / (float)d;
+  const int chunks = a.rot / 2 / v + (d - a.rot + 2 * v - 1) / (2 * v);
+  const bool wide = chunks > 32;
   a.lanes = 1;
   while (a.lanes < 32 && a.lanes < chunks) a.lanes *= 2;
-  a.hpg = 1;
-  a.blocks = (Hq + Hkv + a.hpg - 1) / a.hpg;
+  // as many heads a group as leave two groups for every place on the GPU (2048 threads per SM): the sines cost as
+  // much as two to three heads' memory time, and a call of few rows is over sooner with a head each
+  const int64_t heads = Hq + Hkv, places = (int64_t)tq::sm_count() * 2048 / a.lanes;
+  a.hpg = wide ? 1 : (int)std::min<int64_t>(16, std::max<int64_t>(1, n_tok * heads / (2 * places)));
+  a.blocks = (int)tq::ceil_div(heads, a.hpg);
+  a.hpg = (int)tq::ceil_div(heads, a.blocks);  // even shares
   a.items = n_tok * a.blocks;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   int e;
-  if (dt == TQ_F32) e = v == 4 ? launch<float, 4>(a, pairs, st) : launch<float, 1>(a, pairs, st);
+  if (dt == TQ_F32) e = v == 4 ? launch<float, 4>(a, pairs, wide, st) : launch<float, 1>(a, pairs, wide, st);
   else if (dt == TQ_F16)
-    e = v == 8 ? launch<__half, 8>(a, pairs, st) : v == 4 ? launch<__half, 4>(a, pairs, st) : launch<__half, 1>(a, pairs, st);
+    e = v == 8 ? launch<__half, 8>(a, pairs, wide, st) : v == 4 ? launch<__half, 4>(a, pairs, wide, st) : launch<__half, 1>(a, pairs, wide, st);
   else
-    e = v == 8 ? launch<__nv_bfloat16, 8>(a, pairs, st)
-               : v == 4 ? launch<__nv_bfloat16, 4>(a, pairs, st) : launch<__nv_bfloat16, 1>(a, pairs, st);
+    e = v == 8 ? launch<__nv_bfloat16, 8>(a, pairs, wide, st)
+               : v == 4 ? launch<__nv_bfloat16, 4>(a, pairs, wide, st) : launch<__nv_bfloat16, 1>(a, pairs, wide, st);
   return e == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
 }
