@@ -23,7 +23,9 @@ inline bool al256(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 255u
 constexpr float kQMax = 5548000.0f;
 
 // P_j of the tensor-core kernel's scores: x / 2^j as an integer.
-__device__ __forceinline__ int place_value(float x, int j) { return __float2int_rn(x * (1.f / (float)(1 << j))); }
+__device__ __forceinline__ int place_value(float x, int j) {
+  return __float2int_rn(x * __int_as_float((127 - j) << 23));
+}
 
 // Byte `piece` (0: hi, 1: mid, 2: lo) of v = 2^16 hi + 2^8 mid + lo, |v| <= 127 * 2^16, all three in [-128, 127].
 __device__ __forceinline__ uint32_t digit(int v, int piece) {
@@ -33,50 +35,120 @@ __device__ __forceinline__ uint32_t digit(int v, int piece) {
   return (uint32_t)((piece == 0 ? (v1 - mid) >> 8 : piece == 1 ? mid : lo) & 0xff);
 }
 
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// A head's numbers in fixed point, by a warp (A32 of them a lane, n in all, 32 a + lane): place values to `p`, and the
+// score constants c[0] = 2 w / inv, c[1] = -w k / inv times the sum of what the place values hold (NaN where an entry is
+// not finite; the images are then 0).
+template <int A32>
+__device__ __forceinline__ void fixed_point(const float (&x)[A32], int n, float w, float k, int* p, float* c, int lane) {
+  const int in_byte = n == 64 ? 3 : 7;  // coordinate j is bit j & in_byte of its byte (or half byte)
+  float mx = 1e-30f, bad = 0.f;
+#pragma unroll
+  for (int a = 0; a < A32; ++a)
+    if (32 * a < n) {
+      mx = fmaxf(mx, fabsf(x[a]));
+      bad = fmaf(x[a], 0.f, bad);
+    }
+  mx = warp_max(mx);
+  bad = warp_sum(bad);
+  const float inv = bad == 0.f ? kQMax / mx : 0.f;
+  int sum = 0;  // |sum| < d_pad (kQMax + 2^6) < 2^31
+#pragma unroll
+  for (int a = 0; a < A32; ++a)
+    if (32 * a < n) {
+      const int v = place_value(x[a] * inv, lane & in_byte);
+      p[32 * a + lane] = v;
+      sum += v << (lane & in_byte);
+    }
+  sum = __reduce_add_sync(0xffffffffu, sum);
+  if (lane == 0) {
+    const float u = w * (mx / kQMax);
+    c[0] = 2.f * u;
+    c[1] = bad == 0.f ? -u * k * (float)sum : bad;
+  }
+}
+
 // Block (b, h): q' = H D q / sqrt(d_pad) and u = S q' of the query heads of KV
 // head h, and, for h = 0, the blocks of the sequences before b.  With NT tiles
 // of heads the images that the tensor-core kernel takes (its B operands, thread
 // by thread, and four constants per head), with NT = 0 q' and u.
 //
-// u takes d_pad m G products from S (64 KB at d_pad = m = 128, in L2 after the
-// first block): a thread has one row and a part of the coordinates, so that
-// its loads of S are in flight together.
+// A call of few sequences waits for this kernel's latency, so everything is
+// spread over the block: a warp per head rotates and takes the fixed point, u's
+// products (d_pad m G of them, S 32 KB in fp16 at d_pad = m = 128) go to the
+// tensor cores, a warp per 16 rows of S with all its loads in flight, and a
+// warp per (step, tile) writes images.  q' is scaled by a power of two and split
+// into two halves of 11 bits (S is exact in fp16): u is off by 2^-23 of q' s
+// largest entry times |S row|, and by fp32 sums.
 template <int A32, int NT>
 __global__ void __launch_bounds__(512) queries_kernel(const AttnArgs A, const QParams kq, float alpha_sum) {
-  constexpr int dp = 32 * A32;
-  __shared__ float qs[kMaxGroup][dp];
-  __shared__ float us[NT ? kMaxGroup : 1][NT ? dp : 1];  // m <= d_pad there
-  __shared__ float ps[4][512];
-  __shared__ float inv_s[2][kMaxGroup];
+  constexpr int dp = 32 * A32, LD = dp + 8, HN = 4 * NT, NQ = NT + 1;
+  __shared__ __align__(16) __half qh[2 * kMaxGroup][LD];       // columns 2 h, 2 h + 1: the halves of head h
+  __shared__ int pq[NT ? kMaxGroup : 1][NT ? dp : 1];          // place values of q'
+  __shared__ float unit[kMaxGroup];
   __shared__ long long s_sum[16];
+  // u, and then its place values, in the halves' place (m <= d_pad there)
+  float (*us)[dp] = reinterpret_cast<float (*)[dp]>(&qh[0][0]);
+  static_assert(sizeof(float) * kMaxGroup * dp <= sizeof(qh), "u fits");
   let_next_start();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, tig = lane & 3;
   const int b = blockIdx.x / A.L.hkv, h = blockIdx.x % A.L.hkv;
-  const int m = kq.m;
+  const int m = kq.m, steps = A32 + m / 32, groups = A.hv / A.L.hkv;
+  const int n_tiles = (A.G + 3) / 4;
+  const int64_t row0 = (int64_t)b * A.Hq + (int64_t)h * A.G;
+  uint32_t* const f0 = A.frag + ((int64_t)b * A.hv + (int64_t)h * groups) * A.frag_words;
+  auto constants = [&](int head) {  // of a head: four floats
+    const int grp = head / A.gh;
+    return reinterpret_cast<float*>(f0 + (int64_t)grp * A.frag_words + steps * NQ * 64) + 4 * (head - grp * A.gh);
+  };
+  if (warp < 4 * n_tiles) {  // at most 16
+    float v[A32] = {};
+    if (warp < A.G) {
+      const int64_t at = b * A.q_ld + (int64_t)(h * A.G + warp) * kq.d;
+#pragma unroll
+      for (int a = 0; a < A32; ++a) {
+        const int j = 32 * a + lane;
+        v[a] = j < kq.d ? load_q(A, at + j) : 0.f;
+      }
+      apply_signs<A32>(v, kq.dmask, lane);
+      warp_fwht<A32>(v, lane);
+    }
+    float mx = 0.f;
+#pragma unroll
+    for (int a = 0; a < A32; ++a) {
+      v[a] *= kq.inv_sqrt_dpad;
+      mx = fmaxf(mx, fabsf(v[a]));
+      if (NT == 0 && warp < A.G) A.qrot[(row0 + warp) * dp + 32 * a + lane] = v[a];
+    }
+    mx = warp_max(mx);
+    // 2^e above mx, within what has a reciprocal
+    const int e = min(max((__float_as_int(mx) >> 23) + 1, 27), 253);
+    const float up = __int_as_float(e << 23), down = __int_as_float((254 - e) << 23);
+    if (lane == 0) unit[warp] = up;
+#pragma unroll
+    for (int a = 0; a < A32; ++a) {
+      const float x = v[a] * down;
+      const __half hi = __float2half_rn(x);
+      qh[2 * warp][32 * a + lane] = hi;
+      qh[2 * warp + 1][32 * a + lane] = __float2half_rn(x - __half2float(hi));
+    }
+    if constexpr (NT > 0)
+      if (warp < A.G) fixed_point<A32>(v, dp, A.scale2, alpha_sum, pq[warp], constants(warp), lane);
+  }
   if (h == 0) {
     long long sum = 0;
     for (int i = tid; i < b; i += 512) sum += blocks_of(A, i);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane == 0) s_sum[warp] = sum;
-  }
-  const int64_t row0 = (int64_t)b * A.Hq + (int64_t)h * A.G;
-  for (int g = warp; g < A.G; g += 16) {
-    const int64_t at = b * A.q_ld + (int64_t)(h * A.G + g) * kq.d;
-    float v[A32];
-#pragma unroll
-    for (int a = 0; a < A32; ++a) {
-      const int j = 32 * a + lane;
-      v[a] = j < kq.d ? load_q(A, at + j) : 0.f;
-    }
-    apply_signs<A32>(v, kq.dmask, lane);
-    warp_fwht<A32>(v, lane);
-#pragma unroll
-    for (int a = 0; a < A32; ++a) {
-      v[a] *= kq.inv_sqrt_dpad;
-      qs[g][32 * a + lane] = v[a];
-      if (NT == 0) A.qrot[(row0 + g) * dp + 32 * a + lane] = v[a];
-    }
   }
   __syncthreads();
   if (h == 0 && tid == 0) {
@@ -85,95 +157,80 @@ __global__ void __launch_bounds__(512) queries_kernel(const AttnArgs A, const QP
     A.prefix[b] = sum;
     if (b == A.B - 1) A.prefix[A.B] = sum + blocks_of(A, b);
   }
-  const int parts = m < 512 ? 512 / m : 1, len = (dp + parts - 1) / parts;  // of the coordinates
-  for (int g0 = 0; g0 < A.G; g0 += 4) {
-    for (int e = tid; e < m * parts; e += 512) {
-      const int i = e % m, j0 = e / m * len, j1 = min(dp, j0 + len);
-      float acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 32
-      for (int j = j0; j < j1; ++j) {
-        const float s = kq.St[(int64_t)j * m + i];
+  // u: rows 16 r .. of S; a thread's 16 bytes of a row are the K slots of two products, the same in both operands
+  float acc[kMaxGroup / 4][4];
+  for (int r = warp; r < (m + 15) / 16; r += 16) {
+    uint4 s0[A32], s1[A32];
+    const int i0 = 16 * r + g, i1 = i0 + 8;  // m is a multiple of 32
 #pragma unroll
-        for (int g = 0; g < 4; ++g) acc[g] = fmaf(s, qs[min(g0 + g, A.G - 1)][j], acc[g]);
+    for (int a = 0; a < A32; ++a) {
+      s0[a] = *reinterpret_cast<const uint4*>(kq.S16 + (int64_t)i0 * dp + 32 * a + 8 * tig);
+      s1[a] = *reinterpret_cast<const uint4*>(kq.S16 + (int64_t)i1 * dp + 32 * a + 8 * tig);
+    }
+#pragma unroll
+    for (int t = 0; t < kMaxGroup / 4; ++t) {
+      if (t >= n_tiles) break;
+      float (&d)[4] = acc[t];
+      d[0] = d[1] = d[2] = d[3] = 0.f;
+#pragma unroll
+      for (int a = 0; a < A32; ++a) {
+        const uint4 q = *reinterpret_cast<const uint4*>(&qh[8 * t + g][32 * a + 8 * tig]);
+        mma_f16(d, s0[a].x, s1[a].x, s0[a].y, s1[a].y, q.x, q.y);
+        mma_f16(d, s0[a].z, s1[a].z, s0[a].w, s1[a].w, q.z, q.w);
       }
-      if (parts > 1) {
-#pragma unroll
-        for (int g = 0; g < 4; ++g) ps[g][e] = acc[g];
-      } else {
-#pragma unroll
-        for (int g = 0; g < 4; ++g)
-          if (g0 + g < A.G) A.u[(row0 + g0 + g) * m + i] = acc[g];
+      if (NT == 0 && 4 * t + tig < A.G) {
+        A.u[(row0 + 4 * t + tig) * m + i0] = (d[0] + d[1]) * unit[4 * t + tig];
+        A.u[(row0 + 4 * t + tig) * m + i1] = (d[2] + d[3]) * unit[4 * t + tig];
       }
     }
-    __syncthreads();
-    if (parts > 1) {
-      for (int e = tid; e < 4 * m; e += 512) {
-        const int g = e / m, i = e - g * m;
-        float s = 0.f;
-        for (int p = 0; p < parts; ++p) s += ps[g][p * m + i];
-        if (g0 + g < A.G) {
-          if (NT == 0) A.u[(row0 + g0 + g) * m + i] = s;
-          else us[g0 + g][i] = s;
-        }
-      }
-    }
-    __syncthreads();
   }
   if constexpr (NT > 0) {
-    constexpr int HN = 4 * NT, NQ = NT + 1;
-    const int steps = A32 + m / 32, groups = A.hv / A.L.hkv;
-    uint32_t* f0 = A.frag + ((int64_t)b * A.hv + (int64_t)h * groups) * A.frag_words;
-    // a warp per (q' or u, head): the fixed point's unit, and the sum of what it holds
-    for (int e = warp; e < 2 * groups * HN; e += 16) {
-      const int which = e / (groups * HN), hh = e - which * groups * HN;
-      const int grp = hh / HN, slot = hh - grp * HN, head = grp * A.gh + slot;
-      const bool there = slot < A.gh && head < A.G;
-      const float* x = which ? us[there ? head : 0] : qs[there ? head : 0];
-      const int n = which ? m : dp;
-      const int in_byte = n == 64 ? 3 : 7;  // coordinate j is bit j & in_byte of its byte (or half byte)
-      float mx = 1e-30f, bad = 0.f;
-      for (int j = lane; j < n; j += 32) {
-        mx = fmaxf(mx, fabsf(x[j]));
-        bad = fmaf(x[j], 0.f, bad);  // NaN once an entry is not finite
-      }
-      mx = warp_max(mx);
-      bad = warp_sum(bad);
-      const float inv = bad == 0.f ? kQMax / mx : 0.f;
-      int sum = 0;  // |sum| < d_pad (kQMax + 2^6) < 2^31
-      for (int j = lane; j < n; j += 32) sum += place_value(x[j] * inv, j & in_byte) << (j & in_byte);
-      sum = __reduce_add_sync(0xffffffffu, sum);
-      if (lane == 0) {
-        if (there) inv_s[which][head] = inv;
-        const float w = A.scale2 * (which ? kq.kappa : 1.f) * (mx / kQMax);
-        float* c = reinterpret_cast<float*>(f0 + (int64_t)grp * A.frag_words + steps * NQ * 64) + 4 * slot + 2 * which;
-        c[0] = there ? 2.f * w : 0.f;
-        c[1] = !there ? 0.f : bad == 0.f ? -w * (which ? 1.f : alpha_sum) * (float)sum : bad;
-      }
+    __syncthreads();  // the halves have been read; m <= 256: a warp has had 16 rows at most
+    if (warp < m / 16) {
+#pragma unroll
+      for (int t = 0; t < kMaxGroup / 4; ++t)
+        if (t < n_tiles) {
+          us[4 * t + tig][16 * warp + g] = (acc[t][0] + acc[t][1]) * unit[4 * t + tig];
+          us[4 * t + tig][16 * warp + g + 8] = (acc[t][2] + acc[t][3]) * unit[4 * t + tig];
+        }
     }
     __syncthreads();
-    for (int e = tid; e < groups * steps * NQ * 64; e += 512) {
-      const int r = e & 1, ln = (e >> 1) & 31, t = (e >> 6) % NQ, at = (e >> 6) / NQ;
-      const int grp = at / steps, step = at - grp * steps;
-      const int g = ln >> 2, tig = ln & 3;
+    if (warp < A.G) {
+      float v[A32];
+#pragma unroll
+      for (int a = 0; a < A32; ++a) v[a] = 32 * a < m ? us[warp][32 * a + lane] : 0.f;
+      fixed_point<A32>(v, m, A.scale2 * kq.kappa, 1.f, reinterpret_cast<int*>(us[warp]), constants(warp) + 2, lane);
+    }
+    // places of a last group that no head has
+    for (int e = A.G + tid; e < groups * A.gh; e += 512)
+      *reinterpret_cast<float4*>(constants(e)) = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int e = A.gh + tid; e < HN; e += 512)  // and of a group of fewer than HN
+      for (int grp = 0; grp < groups; ++grp)
+        *reinterpret_cast<float4*>(f0 + (int64_t)grp * A.frag_words + steps * NQ * 64 + 4 * e) = make_float4(0.f, 0.f, 0.f, 0.f);
+    __syncthreads();
+    // images: a warp per (group, step, tile)
+    for (int e = warp; e < groups * steps * NQ; e += 16) {
+      const int t = e % NQ, at = e / NQ, grp = at / steps, step = at - grp * steps;
       const int slot = t < NT ? 4 * t + (g >> 1) : (g >> 1) + 4 * (g & 1), piece = t < NT ? g & 1 : 2;
       const int head = grp * A.gh + slot;
-      uint32_t w = 0;
+      uint32_t w[2] = {0, 0};
       if (slot < A.gh && head < A.G) {
         const bool which = step >= A32;
         const int n = which ? m : dp, st = which ? step - A32 : step;
         // the product of k low bits of the bytes of the thread's word; in two-word planes two threads share one
-        const int k = n == 64 ? 2 * st + 1 + r : (st & 3) + 1 + 4 * r, top = n == 64 ? 4 : 8;
-        const int j0 = n == 64 ? 32 * (tig & 1) + 4 * (tig >> 1) : 32 * (tig + (st & ~3));
-        const float* x = which ? us[head] : qs[head];
-        const float inv = inv_s[which][head];
+        const int top = n == 64 ? 4 : 8;
+        const int* p = (which ? reinterpret_cast<const int*>(us[head]) : pq[head]) +
+                       (n == 64 ? 32 * (tig & 1) + 4 * (tig >> 1) : 32 * (tig + (st & ~3)));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float* xi = x + j0 + 8 * i;
-          const int p = place_value(xi[k - 1] * inv, k - 1);
-          w |= digit(k < top ? p - place_value(xi[k] * inv, k) : p, piece) << (8 * i);
+        for (int r = 0; r < 2; ++r) {
+          const int k = n == 64 ? 2 * st + 1 + r : (st & 3) + 1 + 4 * r;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            w[r] |= digit(p[8 * i + k - 1] - (k < top ? p[8 * i + k] : 0), piece) << (8 * i);
         }
       }
-      f0[(int64_t)grp * A.frag_words + (step * NQ + t) * 64 + 2 * ln + r] = w;
+      reinterpret_cast<uint2*>(f0 + (int64_t)grp * A.frag_words)[(at - grp * steps) * NQ * 32 + t * 32 + lane] =
+          make_uint2(w[0], w[1]);
     }
   }
 }

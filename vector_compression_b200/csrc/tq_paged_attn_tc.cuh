@@ -48,7 +48,14 @@ struct Shape {
   static constexpr int KB = 32 * NK + 64;        // staged words of a block's keys
   static constexpr int VB = KV * DP + 32 + 8;    // and values: 8 mod 32, so that four blocks are on different banks
   static constexpr int WC = 36;                  // words of a column of weights (32 and a gap)
-  static constexpr int WARP_BYTES = 4 * (4 * KB + 4 * VB + 8 * NT * WC) + 16;
+  // the group's scores (a thread's own four of each block), and then its weights
+  static constexpr int XW = 4 * 32 * 4 * NT;
+  static_assert(XW >= 8 * NT * WC, "the weights fit the scores' place");
+  // the running sums: in shared memory the loop over coordinates need not be unrolled (a fourth of the code, which a
+  // short call fetches for one use) and 16 registers a tile are free; at d_pad 256 two warps an SM would not fit
+  static constexpr bool O_SMEM = DP < 256;
+  static constexpr int OW = O_SMEM ? DP / 32 * 32 * 4 * NT : 0;
+  static constexpr int WARP_BYTES = 4 * (4 * KB + 4 * VB + XW + OW) + 16;
   static constexpr int WARPS = 2;
   static constexpr int SMEM = WARPS * WARP_BYTES;
   // resident CTAs: the shared memory's limit, and the registers'
@@ -144,7 +151,9 @@ __global__ void __launch_bounds__(64, Shape<KK, KV, NT, DP, MQ>::CTAS)
   uint32_t* kb = reinterpret_cast<uint32_t*>(smem + warp * S::WARP_BYTES);
   uint32_t* vb = kb + 4 * S::KB;
   uint32_t* wb = vb + 4 * S::VB;
-  const uint32_t bar_k = smem_at(wb + 8 * NT * S::WC), bar_v = bar_k + 8;
+  float4* xs = reinterpret_cast<float4*>(wb) + lane;             // [4 blocks][NT][lanes]
+  float4* os = reinterpret_cast<float4*>(wb + S::XW) + lane;     // [DP / 32][NT][lanes]
+  const uint32_t bar_k = smem_at(wb + S::XW + S::OW), bar_v = bar_k + 8;
   if (lane == 0) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar_k));
     asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar_v));
@@ -228,14 +237,25 @@ __global__ void __launch_bounds__(64, Shape<KK, KV, NT, DP, MQ>::CTAS)
   const int ksh = WPP == 2 ? 4 * (tig >> 1) : 0, ssh = MQ == 64 ? 4 * (tig >> 1) : 0;
 
   float m_run[NT], l_run[NT], w_run[NT];
-  float o[NT][DP / 32][4];  // head 4 nt + tig, coordinates 32 c + 4 g + e
+  float4 o[S::O_SMEM ? 1 : DP / 32][NT];  // head 4 nt + tig, coordinates 32 c + 4 g ..
+  auto o_get = [&](int c, int n) -> float4 {
+    if constexpr (S::O_SMEM) return os[(c * NT + n) * 32];
+    else return o[c][n];
+  };
+  auto o_put = [&](int c, int n, float4 v) {
+    if constexpr (S::O_SMEM) os[(c * NT + n) * 32] = v;
+    else o[c][n] = v;
+  };
+  auto start_sums = [&]() {
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    m_run[n] = -INFINITY;
-    l_run[n] = w_run[n] = 0.f;
+    for (int n = 0; n < NT; ++n) {
+      m_run[n] = -INFINITY;
+      l_run[n] = w_run[n] = 0.f;
 #pragma unroll
-    for (int c = 0; c < DP / 32; ++c) o[n][c][0] = o[n][c][1] = o[n][c][2] = o[n][c][3] = 0.f;
-  }
+      for (int c = 0; c < DP / 32; ++c) o_put(c, n, make_float4(0.f, 0.f, 0.f, 0.f));
+    }
+  };
+  start_sums();
 
   bool ok = true;
   uint32_t phase = 0, k_phase = 0;  // of this group, and of the keys staged last
@@ -253,13 +273,13 @@ __global__ void __launch_bounds__(64, Shape<KK, KV, NT, DP, MQ>::CTAS)
 
     // ---------------- scores, as powers of two
     if (!(ok = __all_sync(0xffffffffu, bounded_wait<true>(bar_k, phase, A.err)))) break;
-    float x[NT][4][4];
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < 4; ++i) {
       const int ni = __shfl_sync(0xffffffffu, nt, i);
+      float x[NT][4];
       if (ni == 0) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) x[n][i][0] = x[n][i][1] = x[n][i][2] = x[n][i][3] = -INFINITY;
+        for (int n = 0; n < NT; ++n) xs[(i * NT + n) * 32] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
         continue;
       }
       const uint32_t* kw = kb + i * S::KB;
@@ -325,8 +345,8 @@ __global__ void __launch_bounds__(64, Shape<KK, KV, NT, DP, MQ>::CTAS)
           }
           const float y1 = n1 * fmaf(r1, fmaf(uc[n].x, whole(acc[FK], 0), uc[n].y), a1);
           const float y2 = n2 * fmaf(r2, fmaf(uc[n].x, whole(acc[FK], 1), uc[n].y), a2);
-          x[n][i][2 * m] = y1;
-          x[n][i][2 * m + 1] = y2;
+          x[n][2 * m] = y1;
+          x[n][2 * m + 1] = y2;
         }
       }
       if (ni < 32) {  // slots without a token hold anything
@@ -334,8 +354,10 @@ __global__ void __launch_bounds__(64, Shape<KK, KV, NT, DP, MQ>::CTAS)
         for (int r = 0; r < 4; ++r)
           if (16 * th + 4 * (r ^ th) + ts >= ni)
 #pragma unroll
-            for (int n = 0; n < NT; ++n) x[n][i][r] = -INFINITY;
+            for (int n = 0; n < NT; ++n) x[n][r] = -INFINITY;
       }
+#pragma unroll
+      for (int n = 0; n < NT; ++n) xs[(i * NT + n) * 32] = make_float4(x[n][0], x[n][1], x[n][2], x[n][3]);
     }
     __syncwarp();  // the keys have been read
     if (!done) {
@@ -345,6 +367,18 @@ __global__ void __launch_bounds__(64, Shape<KK, KV, NT, DP, MQ>::CTAS)
 
     // ---------------- weights
     if (!(ok = __all_sync(0xffffffffu, bounded_wait<true>(bar_v, phase, A.err)))) break;
+    float x[NT][4][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 v = xs[(i * NT + n) * 32];
+        x[n][i][0] = v.x;
+        x[n][i][1] = v.y;
+        x[n][i][2] = v.z;
+        x[n][i][3] = v.w;
+      }
+    __syncwarp();  // the scores' place is the weights' from here on
     float back[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -376,9 +410,10 @@ __global__ void __launch_bounds__(64, Shape<KK, KV, NT, DP, MQ>::CTAS)
         l_run[n] *= corr;
         if (KV == 4) w_run[n] *= corr;
 #pragma unroll
-        for (int c = 0; c < DP / 32; ++c)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[n][c][e] *= corr;
+        for (int c = 0; c < DP / 32; ++c) {
+          const float4 t = o_get(c, n);
+          o_put(c, n, make_float4(t.x * corr, t.y * corr, t.z * corr, t.w * corr));
+        }
       }
       l_run[n] += l;
       if (KV == 4) w_run[n] += wsum;
@@ -412,7 +447,7 @@ __global__ void __launch_bounds__(64, Shape<KK, KV, NT, DP, MQ>::CTAS)
       bw[n][3] = make_uint2(b.z, b.w);
     }
     const uint32_t* vw = vb + tig * S::VB + 4 * g;
-#pragma unroll
+#pragma unroll S::O_SMEM ? 1 : DP / 32
     for (int c = 0; c < DP / 32; ++c) {
       uint32_t w[4][KV];
 #pragma unroll
@@ -450,15 +485,18 @@ __global__ void __launch_bounds__(64, Shape<KK, KV, NT, DP, MQ>::CTAS)
           }
         }
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            // in units of 2^8: what the shift drops is below 2^-8 of a unit, of 2^30 where the weights are large
-            const int v = 256 * ah[mt][n][2 * r] + ah[mt][n][2 * r + 1] + al[mt][n][2 * r] + (al[mt][n][2 * r + 1] >> 8);
-            o[n][c][2 * mt + r] = fmaf(back[n], (float)v, o[n][c][2 * mt + r]);
-          }
+      for (int n = 0; n < NT; ++n) {
+        // in units of 2^8: what the shift drops is below 2^-8 of a unit, of 2^30 where the weights are large
+        auto sum = [&](int mt, int r) {
+          return (float)(256 * ah[mt][n][2 * r] + ah[mt][n][2 * r + 1] + al[mt][n][2 * r] + (al[mt][n][2 * r + 1] >> 8));
+        };
+        float4 t = o_get(c, n);
+        t.x = fmaf(back[n], sum(0, 0), t.x);
+        t.y = fmaf(back[n], sum(0, 1), t.y);
+        t.z = fmaf(back[n], sum(1, 0), t.z);
+        t.w = fmaf(back[n], sum(1, 1), t.w);
+        o_put(c, n, t);
+      }
     }
     __syncwarp();  // values and weights have been read
     if (!done) stage(nat, false);
@@ -479,15 +517,13 @@ __global__ void __launch_bounds__(64, Shape<KK, KV, NT, DP, MQ>::CTAS)
           // four-bit levels stand half a step low (their negatives are complements)
           const float up = KV == 4 ? 0.5f * K.unit * ws : 0.f;
 #pragma unroll
-          for (int c = 0; c < DP / 32; ++c)
-            *reinterpret_cast<float4*>(pp + 4 + 32 * c + 4 * g) =
-                make_float4(o[n][c][0] + up, o[n][c][1] + up, o[n][c][2] + up, o[n][c][3] + up);
+          for (int c = 0; c < DP / 32; ++c) {
+            const float4 t = o_get(c, n);
+            *reinterpret_cast<float4*>(pp + 4 + 32 * c + 4 * g) = make_float4(t.x + up, t.y + up, t.z + up, t.w + up);
+          }
         }
-        m_run[n] = -INFINITY;
-        l_run[n] = w_run[n] = 0.f;
-#pragma unroll
-        for (int c = 0; c < DP / 32; ++c) o[n][c][0] = o[n][c][1] = o[n][c][2] = o[n][c][3] = 0.f;
       }
+      start_sums();
       if (!done) queries(nx);
     }
     if (done) break;
