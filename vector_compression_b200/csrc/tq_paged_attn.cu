@@ -76,7 +76,7 @@ __device__ __forceinline__ void fixed_point(const float (&x)[A32], int n, float 
 }
 
 // Block (b, h): q' = H D q / sqrt(d_pad) and u = S q' of the query heads of KV
-// head h, and, for h = 0, the blocks of the sequences before b.  With NT tiles
+// head h, and, for h = 0, the units of the sequences before b.  With NT tiles
 // of heads the images that the tensor-core kernel takes (its B operands, thread
 // by thread, and four constants per head), with NT = 0 q' and u.
 //
@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(512) queries_kernel(const AttnArgs A, const QP
   }
   if (h == 0) {
     long long sum = 0;
-    for (int i = tid; i < b; i += 512) sum += blocks_of(A, i);
+    for (int i = tid; i < b; i += 512) sum += units_of(A, i);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane == 0) s_sum[warp] = sum;
@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(512) queries_kernel(const AttnArgs A, const QP
     long long sum = 0;
     for (int i = 0; i < 16; ++i) sum += s_sum[i];
     A.prefix[b] = sum;
-    if (b == A.B - 1) A.prefix[A.B] = sum + blocks_of(A, b);
+    if (b == A.B - 1) A.prefix[A.B] = sum + units_of(A, b);
   }
   // u: rows 16 r .. of S; a thread's 16 bytes of a row are the K slots of two products, the same in both operands
   float acc[kMaxGroup / 4][4];
@@ -270,12 +270,12 @@ __global__ void __launch_bounds__(128) attention_any_kernel(const AttnArgs A, co
   }
   wait_for_previous();
   let_next_start();
-  const int64_t units = A.prefix[A.B] * L.hkv, share = share_of(A, units);
-  int64_t u0 = blockIdx.x * share;
-  const int64_t u1 = min64(units, u0 + share);
+  const int64_t units = A.prefix[A.B] * L.hkv;
+  int64_t u0 = share_at(A, units, blockIdx.x);
+  const int64_t u1 = share_at(A, units, blockIdx.x + 1);
   while (u0 < u1) {
     const Segment sg = segment_at(A, u0, u1, lane);
-    u0 += sg.end - sg.blk;
+    u0 += (sg.end - sg.blk + kUnit - 1) / kUnit;
     const int64_t row0 = (int64_t)sg.b * A.Hq + (int64_t)sg.h * G;
     __syncthreads();
     for (int e = tid; e < G * dp; e += 128) qs[e] = A.qrot[row0 * dp + e];
@@ -399,10 +399,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const AttnArgs A,
   wait_for_previous();
   const int64_t p0 = A.prefix[b];
   const int64_t n = A.prefix[b + 1] - p0;
-  const int64_t share = share_of(A, A.prefix[A.B] * A.hv);
+  const int64_t units = A.prefix[A.B] * A.hv;
   const int64_t s0 = A.hv * p0 + h * n, bh = (int64_t)b * A.hv + h;
   // parts c0 .. c1; none of an empty sequence
-  const int c0 = (int)(s0 / share), c1 = n ? (int)((s0 + n - 1) / share) : c0 - 1;
+  const int c0 = n ? worker_of(A, units, s0) : 0, c1 = n ? worker_of(A, units, s0 + n - 1) : -1;
   float top = -INFINITY;
   for (int c = c0 + tid; c <= c1; c += 32 * kJoinWarps) top = fmaxf(top, slot_of(A, bh, c, g)[0]);
   top = warp_max(top);

@@ -2,15 +2,17 @@
 // join of its parts.
 //
 // The query heads of a KV head are taken in groups of at most `gh`; a KV head
-// with its group is a virtual head, `hv` per sequence.  The blocks of 32 tokens
-// of all sequences and virtual heads, in the order (sequence, virtual head,
-// block), are one line of U units, cut into equal shares, one per worker (a
-// warp or a CTA), whatever the sequences' lengths; so a long sequence is spread
-// over many workers and a worker may hold several short ones.  What a worker
-// has of one (sequence, virtual head) is a segment; it leaves the partial
-// (m, l, o) of each of its segments in the workspace, m as a power of two's
-// exponent.  Segment (bh, worker c) has slot bh + c: from one segment to the
-// next bh or c or both grow, so no two share a slot.
+// with its group is a virtual head, `hv` per sequence.  A unit is 4 blocks of 32
+// tokens (fewer at a sequence's end) of one virtual head: what a warp's value
+// pass takes at a time.  The units of all sequences and virtual heads, in the
+// order (sequence, virtual head, blocks), are one line, cut into equal shares
+// (within one unit), one per worker (a warp or a CTA), whatever the sequences'
+// lengths; so a long sequence is spread over many workers and a worker may hold
+// several short ones.  What a worker has of one (sequence, virtual head) is a
+// segment; it leaves the partial (m, l, o) of each of its segments in the
+// workspace, m as a power of two's exponent.  Segment (bh, worker c) has slot
+// bh + c: from one segment to the next bh or c or both grow, so no two share a
+// slot.
 #pragma once
 
 #include "tq_device.cuh"
@@ -19,7 +21,7 @@
 namespace tq {
 namespace paged {
 
-constexpr int kMinShare = 4;  // blocks: what a warp's value pass takes at a time
+constexpr int kUnit = 4;       // blocks
 constexpr int kMaxGroup = 16; // query heads per KV head
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -38,7 +40,7 @@ struct AttnArgs {
   void* out;
   float* lse;
   int workers;           // of the main kernel
-  int64_t* prefix;       // [B + 1]: blocks of the sequences before b
+  int64_t* prefix;       // [B + 1]: units a head of the sequences before b
   float* qrot;           // [B * Hq][d_pad] (the kernel for any shape)
   float* u;              // [B * Hq][m]
   uint32_t* frag;        // [B * hv] query images (the tensor-core kernel)
@@ -47,13 +49,18 @@ struct AttnArgs {
   unsigned* err;
 };
 
-__device__ __forceinline__ int64_t share_of(const AttnArgs& A, int64_t units) {
-  const int64_t s = (units + A.workers - 1) / A.workers;
-  return s < kMinShare ? kMinShare : s;
+// Worker c's share of `units` is [share_at(c), share_at(c + 1)): none is empty below min(units, workers).
+__device__ __forceinline__ int64_t share_at(const AttnArgs& A, int64_t units, int64_t c) {
+  const int64_t w = min64(units, A.workers);
+  return c >= w ? units : c * units / w;
+}
+// The worker whose share unit x is in: the last c with c units / w < x + 1.
+__device__ __forceinline__ int worker_of(const AttnArgs& A, int64_t units, int64_t x) {
+  return (int)(((x + 1) * min64(units, A.workers) - 1) / units);
 }
 
-__device__ __forceinline__ int blocks_of(const AttnArgs& A, int64_t b) {
-  return (clamp_len(A.lens[b], A.L, A.tab.max_pages) + 31) / 32;
+__device__ __forceinline__ int units_of(const AttnArgs& A, int64_t b) {
+  return (clamp_len(A.lens[b], A.L, A.tab.max_pages) + 32 * kUnit - 1) / (32 * kUnit);
 }
 
 struct Segment {
@@ -62,19 +69,20 @@ struct Segment {
   int len;             // tokens of the sequence
 };
 
-// The segment that begins n_units before the share's end at unit `rel` of sequence b, which has nb blocks a head.
-__device__ __forceinline__ Segment segment_in(const AttnArgs& A, int b, int nb, int64_t rel, int64_t n_units) {
+// The segment from unit `rel` of sequence b on, which has n units a head, for a share of `left` more units.
+__device__ __forceinline__ Segment segment_in(const AttnArgs& A, int b, int n, int64_t rel, int64_t left) {
   Segment s;
   s.b = b;
-  s.h = (int)(rel / nb);
+  s.h = (int)(rel / n);
   s.kvh = s.h / (A.hv / A.L.hkv);
-  s.blk = (int)(rel - (int64_t)s.h * nb);
-  s.end = (int)min64(nb, s.blk + n_units);
   s.len = clamp_len(A.lens[b], A.L, A.tab.max_pages);
+  const int first = (int)(rel - (int64_t)s.h * n);
+  s.blk = kUnit * first;
+  s.end = (int)min64((s.len + 31) / 32, kUnit * (first + min64(n, left)));
   return s;
 }
 
-// The segment that unit u0 begins, cut at u1, found in the blocks' prefix sums; called by a whole warp.
+// The segment that unit u0 begins, cut at u1, found in the units' prefix sums; called by a whole warp.
 __device__ __forceinline__ Segment segment_at(const AttnArgs& A, int64_t u0, int64_t u1, int lane) {
   const int64_t x = u0 / A.hv;
   int lo = 0, n = A.B;  // the last b with prefix[b] <= x is in [lo, lo + n)
@@ -89,48 +97,48 @@ __device__ __forceinline__ Segment segment_at(const AttnArgs& A, int64_t u0, int
   return segment_in(A, lo, (int)(A.prefix[lo + 1] - p), u0 - A.hv * p, u1 - u0);
 }
 
-// The segment behind s, for a share that goes on to u1; u0 is its first unit.
+// The segment behind s, for a share that goes on from unit u0 to u1.
 __device__ __forceinline__ Segment segment_after(const AttnArgs& A, const Segment& s, int64_t u0, int64_t u1) {
-  int b = s.b, nb = blocks_of(A, b);
-  int64_t rel = (int64_t)(s.h + 1) * nb;
+  int b = s.b, n = units_of(A, b);
+  int64_t rel = (int64_t)(s.h + 1) * n;
   if (s.h + 1 == A.hv) {
     rel = 0;
-    do nb = blocks_of(A, ++b);
-    while (nb == 0);  // ends: a unit u0 < u1 <= units is some sequence's
+    do n = units_of(A, ++b);
+    while (n == 0);  // ends: a unit u0 < u1 <= units is some sequence's
   }
-  return segment_in(A, b, nb, rel, u1 - u0);
+  return segment_in(A, b, n, rel, u1 - u0);
 }
 
-// Up to this many sequences a warp sums their blocks itself, and need not wait for the prefix sums.
+// Up to this many sequences a warp sums their units itself, and need not wait for the prefix sums.
 constexpr int kOwnSums = 1024;
 
 // A worker's first segment and its share [u0, u1) of the units from the lengths alone; B <= kOwnSums, a whole warp.
 __device__ __forceinline__ Segment first_segment(const AttnArgs& A, int worker, int64_t& u0, int64_t& u1, int lane) {
   const int per = (A.B + 31) / 32, b0 = lane * per, b1 = min(A.B, b0 + per);
   long long mine = 0;
-  for (int b = b0; b < b1; ++b) mine += blocks_of(A, b);
+  for (int b = b0; b < b1; ++b) mine += units_of(A, b);
   long long upto = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const long long x = __shfl_up_sync(0xffffffffu, upto, o);
     if (lane >= o) upto += x;
   }
-  const int64_t units = __shfl_sync(0xffffffffu, upto, 31) * A.hv, share = share_of(A, units);
-  u0 = worker * share;
-  u1 = min64(units, u0 + share);
+  const int64_t units = __shfl_sync(0xffffffffu, upto, 31) * A.hv;
+  u0 = share_at(A, units, worker);
+  u1 = share_at(A, units, worker + 1);
   Segment s = {};
   if (u0 >= u1) return s;
   const long long x = u0 / A.hv, before = upto - mine;
-  // the last lane whose sequences begin at or before x (it has blocks: the next lane's begin behind x)
+  // the last lane whose sequences begin at or before x (it has units: the next lane's begin behind x)
   const int at = __popc(__ballot_sync(0xffffffffu, before <= x)) - 1;
-  int b = at * per, nb = 0;
+  int b = at * per, n = 0;
   long long p = __shfl_sync(0xffffffffu, before, at);
   for (;; ++b) {
-    nb = blocks_of(A, b);
-    if (p + nb > x) break;
-    p += nb;
+    n = units_of(A, b);
+    if (p + n > x) break;
+    p += n;
   }
-  return segment_in(A, b, nb, u0 - A.hv * p, u1 - u0);
+  return segment_in(A, b, n, u0 - A.hv * p, u1 - u0);
 }
 
 __host__ __device__ __forceinline__ int part_row(int dp) { return dp + 4; }  // 16-byte rows

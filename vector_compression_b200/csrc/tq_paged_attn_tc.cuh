@@ -2,7 +2,7 @@
 // for d_pad 64, 128 and 256 (tq_paged_attn.cuh: the split of the work).
 //
 // A warp is a worker: it takes its share of 32-token block records four at a
-// time (a group), keys and values each staged by bulk copies; the next group's
+// time (a unit, here a group), keys and values each staged by bulk copies; the next group's
 // keys load while this one's values are summed, its values while the next keys
 // are scored.  No warp waits for another.
 //
@@ -171,9 +171,9 @@ __global__ void __launch_bounds__(64, Shape<KK, KV, NT, DP, MQ>::CTAS)
     sg = first_segment(A, worker, u, u_end, lane);
   } else {
     wait_for_previous();
-    const int64_t units = A.prefix[A.B] * A.hv, share = share_of(A, units);
-    u = worker * share;
-    u_end = min64(units, u + share);
+    const int64_t units = A.prefix[A.B] * A.hv;
+    u = share_at(A, units, worker);
+    u_end = share_at(A, units, worker + 1);
     if (u < u_end) sg = segment_at(A, u, u_end, lane);
   }
   const int64_t u_first = u;
@@ -262,10 +262,9 @@ __global__ void __launch_bounds__(64, Shape<KK, KV, NT, DP, MQ>::CTAS)
   for (;; phase ^= 1u) {
     // what comes after this group
     Segment nx = sg;
-    const int step = min(4, sg.end - sg.blk);
-    u += step;
-    nx.blk += step;
-    const bool last = nx.blk == sg.end, done = u >= u_end;
+    ++u;
+    nx.blk += kUnit;
+    const bool last = nx.blk >= sg.end, done = u >= u_end;
     if (last && !done) nx = segment_after(A, sg, u, u_end);
     int64_t nat = -1;
     int nnt = 0;
@@ -538,7 +537,7 @@ __global__ void __launch_bounds__(64, Shape<KK, KV, NT, DP, MQ>::CTAS)
     bounded_wait<true>(bar_v, phase, nullptr);
     for (u = u_first; u < u_end;) {
       sg = segment_at(A, u, u_end, lane);
-      u += sg.end - sg.blk;
+      u += (sg.end - sg.blk + kUnit - 1) / kUnit;
       if (lane < A.gh)
         *reinterpret_cast<float2*>(slot_of(A, (int64_t)sg.b * A.hv + sg.h, worker, lane)) = make_float2(-INFINITY, 0.f);
     }
