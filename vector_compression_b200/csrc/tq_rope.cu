@@ -18,6 +18,7 @@
 #include <cmath>
 #include <cstdint>
 #include <new>
+#include <type_traits>
 
 #include "tq_device.cuh"
 #include "tq_internal.h"
@@ -42,38 +43,54 @@ struct Side {  // q or k
 struct Args {
   Side s[2];
   const int64_t* pos;
-  int64_t items;  // (token, block of heads)
+  int64_t items, n_tok;  // (block of heads, token)
   int d, rot, blocks, hpg;  // blocks of hpg heads per token
   int lanes;      // of a group: a power of two
   float eps, mscale, inv_d;
   uint64_t turn[128];
 };
 
-template <typename T>
-__device__ __forceinline__ T from_f32(float v);
-template <>
-__device__ __forceinline__ float from_f32<float>(float v) { return v; }
-template <>
-__device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
-
 template <typename T, int V>
 struct alignas(sizeof(T) * V) Vec {
   T e[V];
 };
 
+__device__ __forceinline__ void unpack2(const float* p, float& a, float& b) { a = p[0], b = p[1]; }
+__device__ __forceinline__ void unpack2(const __half* p, float& a, float& b) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(p));
+  a = f.x, b = f.y;
+}
+__device__ __forceinline__ void unpack2(const __nv_bfloat16* p, float& a, float& b) {
+  const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
+  a = __uint_as_float(w << 16), b = __uint_as_float(w & 0xffff0000u);
+}
+template <typename T, int V>
+__device__ __forceinline__ void unpack(const Vec<T, V>& r, float (&v)[V]) {
+  if constexpr (V == 1) v[0] = to_f32(r.e[0]);
+  else
+#pragma unroll
+    for (int i = 0; i < V; i += 2) unpack2(r.e + i, v[i], v[i + 1]);
+}
+__device__ __forceinline__ void pack2(float* d, float a, float b) { d[0] = a, d[1] = b; }
+__device__ __forceinline__ void pack2(__half* d, float a, float b) { *reinterpret_cast<__half2*>(d) = __floats2half2_rn(a, b); }
+__device__ __forceinline__ void pack2(__nv_bfloat16* d, float a, float b) {
+  *reinterpret_cast<__nv_bfloat162*>(d) = __floats2bfloat162_rn(a, b);
+}
+__device__ __forceinline__ void pack1(float* d, float a) { *d = a; }
+__device__ __forceinline__ void pack1(__half* d, float a) { *d = __float2half_rn(a); }
+__device__ __forceinline__ void pack1(__nv_bfloat16* d, float a) { *d = __float2bfloat16_rn(a); }
+
 template <typename T, int V>
 __device__ __forceinline__ void load(const T* p, float (&v)[V]) {
-  const Vec<T, V> r = *reinterpret_cast<const Vec<T, V>*>(p);
-#pragma unroll
-  for (int i = 0; i < V; ++i) v[i] = to_f32(r.e[i]);
+  unpack(*reinterpret_cast<const Vec<T, V>*>(p), v);
 }
 template <typename T, int V>
 __device__ __forceinline__ void store(T* p, const float (&v)[V]) {
   Vec<T, V> r;
+  if constexpr (V == 1) pack1(r.e, v[0]);
+  else
 #pragma unroll
-  for (int i = 0; i < V; ++i) r.e[i] = from_f32<T>(v[i]);
+    for (int i = 0; i < V; i += 2) pack2(r.e + i, v[i], v[i + 1]);
   *reinterpret_cast<Vec<T, V>*>(p) = r;
 }
 
@@ -91,116 +108,178 @@ __device__ __forceinline__ void chunk_at(int c, int np, const Args& A, int& a, i
   }
 }
 
-// cos and sin (times mscale) of the V pairs of chunk c.
-template <int V>
+// cos and sin (times mscale) of the V pairs of chunk c.  For 16-bit results the
+// hardware's sine of an angle within half a turn is enough: it is off by 2^-21,
+// the result's rounding by 2^-12 or 2^-9.
+template <typename T, int V>
 __device__ __forceinline__ void turns(const Args& A, int c, uint64_t pos, float (&co)[V], float (&si)[V]) {
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     // the top 32 bits of the fraction as a signed number of half turns
-    const int hi = (int)(uint32_t)((pos * A.turn[V * c + i]) >> 32);
-    sincospif((float)hi * 0x1p-31f, &si[i], &co[i]);
+    const float x = (float)(int)(uint32_t)((pos * A.turn[V * c + i]) >> 32);
+    if constexpr (sizeof(T) == 2) {
+      const float y = x * (0x1p-31f * 3.14159265358979f);
+      si[i] = __sinf(y);
+      co[i] = __cosf(y);
+    } else {
+      sincospif(x * 0x1p-31f, &si[i], &co[i]);
+    }
     co[i] *= A.mscale;
     si[i] *= A.mscale;
   }
 }
 
+// Position of pair i of a chunk in its two vectors.
 template <int V, bool PAIRS>
-__device__ __forceinline__ void rotate(float (&x)[V], float (&z)[V], const float (&co)[V], const float (&si)[V]) {
-  if constexpr (!PAIRS) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const float a = x[i], b = z[i];
-      x[i] = a * co[i] - b * si[i];
-      z[i] = b * co[i] + a * si[i];
-    }
+__device__ __forceinline__ void pair_at(float (&x)[V], float (&z)[V], int i, float*& a, float*& b) {
+  if (PAIRS) {  // coordinates 2 i and 2 i + 1 of the 2 V
+    a = 2 * i < V ? &x[2 * i % V] : &z[2 * i % V];
+    b = 2 * i + 1 < V ? &x[(2 * i + 1) % V] : &z[(2 * i + 1) % V];
   } else {
-    float t[2 * V];
+    a = &x[i];
+    b = &z[i];
+  }
+}
+// The factors of a chunk's pairs, (a, b) -> (a f0 - b f1, b f2 + a f3): the weights' (g0, g1) times the turn's.
+template <int V>
+struct Factors {
+  float f0[V], f1[V], f2[V], f3[V];
+};
+template <int V, bool PAIRS>
+__device__ __forceinline__ void rotate(float (&x)[V], float (&z)[V], const Factors<V>& f) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) t[i] = x[i], t[V + i] = z[i];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const float a = t[2 * i], b = t[2 * i + 1];
-      t[2 * i] = a * co[i] - b * si[i];
-      t[2 * i + 1] = b * co[i] + a * si[i];
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i) x[i] = t[i], z[i] = t[V + i];
+  for (int i = 0; i < V; ++i) {
+    float *pa, *pb;
+    pair_at<V, PAIRS>(x, z, i, pa, pb);
+    const float a = *pa, b = *pb;
+    *pa = a * f.f0[i] - b * f.f1[i];
+    *pb = b * f.f2[i] + a * f.f3[i];
   }
 }
 
-// Rows of one side: V pairs (or coordinates that pass) a lane, U heads' loads in flight.
-template <typename T, int V, bool PAIRS, int U>
-__device__ __forceinline__ void norm_rope_rows(const Args& A, const Side& s, int64_t tok, int h0, int h1, int lane,
-                                               unsigned mask, bool there, bool turn, int a, int b, const float (&co)[V],
-                                               const float (&si)[V]) {
-  const T* x = static_cast<const T*>(s.x) + tok * s.xt + a;
-  T* y = static_cast<T*>(s.y) + tok * s.yt + a;
-  const int ab = b - a;
-  float g0[V], g1[V];
-  if (s.w && there) {
-    load<T, V>(static_cast<const T*>(s.w) + a, g0);
-    if (b >= 0) load<T, V>(static_cast<const T*>(s.w) + b, g1);
-  }
-  for (int h = h0; h < h1; h += U) {
-    Vec<T, V> r0[U], r1[U];
+// `n` rows of one side from x and y on, V pairs (or coordinates that pass) a lane, U rows' loads in flight.
+// FULL: every lane has a whole chunk.
+template <typename T, int V, bool PAIRS, bool NORM, bool FULL, int U>
+__device__ __forceinline__ void norm_rope_rows(const Args& A, const T* x, int64_t xh, T* y, int64_t yh, int n, int ab,
+                                               unsigned mask, bool there, bool both, bool turn, const Factors<V>& f) {
+  auto rows = [&](auto count) {
+    constexpr int C = decltype(count)::value;
+    Vec<T, V> r0[C], r1[C];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (there && h + u < h1) {
-        r0[u] = *reinterpret_cast<const Vec<T, V>*>(x + (h + u) * s.xh);
-        if (b >= 0) r1[u] = *reinterpret_cast<const Vec<T, V>*>(x + (h + u) * s.xh + ab);
-      }
+    for (int u = 0; u < C; ++u) {
+      if (!FULL) r0[u] = {}, r1[u] = {};
+      if (FULL || there) r0[u] = *reinterpret_cast<const Vec<T, V>*>(x);
+      if (FULL || both) r1[u] = *reinterpret_cast<const Vec<T, V>*>(x + ab);
+      x += xh;
     }
+    float p[C][V], q[C][V];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (h + u >= h1) break;
-      float p[V], q[V];
+    for (int u = 0; u < C; ++u) {
+      unpack(r0[u], p[u]);
+      unpack(r1[u], q[u]);
+    }
+    if (NORM) {
+      float inv[C];
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        p[i] = there ? to_f32(r0[u].e[i]) : 0.f;
-        q[i] = there && b >= 0 ? to_f32(r1[u].e[i]) : 0.f;
+      for (int u = 0; u < C; ++u) {
+        inv[u] = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) inv[u] = fmaf(p[u][i], p[u][i], fmaf(q[u][i], q[u][i], inv[u]));
       }
-      if (s.w) {
-        float sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < V; ++i) sum = fmaf(p[i], p[i], fmaf(q[i], q[i], sum));
-        for (int o = A.lanes >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(mask, sum, o);
-        const float inv = rsqrtf(sum * A.inv_d + A.eps);
+      for (int o = 16; o > 0; o >>= 1)
+        if (o < A.lanes)
+#pragma unroll
+          for (int u = 0; u < C; ++u) inv[u] += __shfl_xor_sync(mask, inv[u], o);
+#pragma unroll
+      for (int u = 0; u < C; ++u) {
+        inv[u] = rsqrtf(inv[u] * A.inv_d + A.eps);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          p[i] *= inv * g0[i];
-          q[i] *= inv * g1[i];
+          p[u][i] *= inv[u];
+          q[u][i] *= inv[u];
         }
       }
-      if (!there) continue;
-      if (b >= 0) {
-        if (turn) rotate<V, PAIRS>(p, q, co, si);
-        store<T, V>(y + (h + u) * s.yh + ab, q);
-      }
-      store<T, V>(y + (h + u) * s.yh, p);
     }
+#pragma unroll
+    for (int u = 0; u < C; ++u) {
+      if (turn) {
+        rotate<V, PAIRS>(p[u], q[u], f);
+      } else if (NORM) {  // f0 and f2: the weights of the two vectors
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          p[u][i] *= f.f0[i];
+          q[u][i] *= f.f2[i];
+        }
+      }
+      if (FULL || there) store<T, V>(y, p[u]);
+      if (FULL || both) store<T, V>(y + ab, q[u]);
+      y += yh;
+    }
+  };
+  for (; n >= U; n -= U) rows(std::integral_constant<int, U>{});
+  if (U > 2 && n >= 2) {
+    rows(std::integral_constant<int, 2>{});
+    n -= 2;
   }
+  for (; n > 0; --n) rows(std::integral_constant<int, 1>{});
 }
 
 // A group of lanes takes hpg heads of a token, a chunk of the row per lane: the
 // row is read once, and the sines serve all of the heads.
-template <typename T, int V, bool PAIRS>
-__global__ void __launch_bounds__(256) norm_rope_kernel(const __grid_constant__ Args A) {
+template <typename T, int V, bool PAIRS, bool FULL>
+__global__ void __launch_bounds__(256, V == 8 ? 2 : 3) norm_rope_kernel(const __grid_constant__ Args A) {
   const int lane = threadIdx.x & (A.lanes - 1);
   const unsigned mask = (A.lanes == 32 ? 0xffffffffu : ((1u << A.lanes) - 1u)) << ((threadIdx.x & 31) & ~(A.lanes - 1));
   const int64_t item = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / A.lanes;
   if (item >= A.items) return;
-  const int64_t tok = item / A.blocks;
-  const int h0 = (int)(item - tok * A.blocks) * A.hpg, hq = A.s[0].heads;
+  // tokens run fastest: the groups of a warp have the same heads, and take the same turns
+  const int64_t blk = A.items <= 0x7fffffff ? (uint32_t)item / (uint32_t)A.n_tok : item / A.n_tok, tok = item - blk * A.n_tok;
+  const int h0 = (int)blk * A.hpg, hq = A.s[0].heads;
   const int h1 = min(h0 + A.hpg, hq + A.s[1].heads);
   const int np = A.rot / 2 / V, nc = np + (A.d - A.rot + 2 * V - 1) / (2 * V);
   const bool there = lane < nc, turn = lane < np;
   int a = 0, b = -1;
   if (there) chunk_at<V, PAIRS>(lane, np, A, a, b);
-  float co[V] = {}, si[V] = {};
-  if (turn) turns<V>(A, lane, (uint64_t)A.pos[tok], co, si);
-  constexpr int U = V > 1 ? 4 : 2;
-  if (h0 < hq) norm_rope_rows<T, V, PAIRS, U>(A, A.s[0], tok, h0, min(h1, hq), lane, mask, there, turn, a, b, co, si);
-  if (h1 > hq) norm_rope_rows<T, V, PAIRS, U>(A, A.s[1], tok, max(h0, hq) - hq, h1 - hq, lane, mask, there, turn, a, b, co, si);
+  const bool both = b >= 0;
+  const uint64_t pos = turn ? (uint64_t)A.pos[tok] : 0;
+  // rows in flight against registers: four of eight-element vectors at two blocks per SM (16384 x 40 x 128 fp16: 63 us,
+  // with norms 70) or two of the smaller ones at three; two at three blocks are 63 and 75 there, four spill
+  constexpr int U = V == 8 ? 4 : 2;
+#pragma unroll 1
+  for (int side = 0; side < 2; ++side) {
+    const Side& s = A.s[side];
+    const int first = side ? max(h0, hq) - hq : h0, n = (side ? h1 - hq : min(h1, hq)) - first;
+    if (n <= 0) continue;
+    const T* x = static_cast<const T*>(s.x) + tok * s.xt + first * s.xh + a;
+    T* y = static_cast<T*>(s.y) + tok * s.yt + first * s.yh + a;
+    Factors<V> f;
+    float co[V] = {}, si[V] = {};
+    if (turn) turns<T, V>(A, lane, pos, co, si);
+    if (s.w) {
+      float g0[V] = {}, g1[V] = {};
+      if (there) load<T, V>(static_cast<const T*>(s.w) + a, g0);
+      if (both) load<T, V>(static_cast<const T*>(s.w) + b, g1);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        f.f0[i] = g0[i];
+        f.f2[i] = g1[i];
+        if (turn) {
+          float *pa, *pb;
+          pair_at<V, PAIRS>(g0, g1, i, pa, pb);
+          f.f0[i] = *pa * co[i];
+          f.f1[i] = *pb * si[i];
+          f.f2[i] = *pb * co[i];
+          f.f3[i] = *pa * si[i];
+        }
+      }
+      norm_rope_rows<T, V, PAIRS, true, FULL, U>(A, x, s.xh, y, s.yh, n, b - a, mask, there, both, turn, f);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) f.f0[i] = f.f2[i] = co[i], f.f1[i] = f.f3[i] = si[i];
+      norm_rope_rows<T, V, PAIRS, false, FULL, U>(A, x, s.xh, y, s.yh, n, b - a, mask, there, both, turn, f);
+    }
+  }
 }
 
 // Rows of more than 32 chunks (long heads, or no alignment for vectors): a warp per (token, head), chunk by chunk.
@@ -256,8 +335,11 @@ __global__ void __launch_bounds__(256) norm_rope_wide_kernel(const __grid_consta
       }
       if (c < np) {
         float co[V], si[V];
-        turns<V>(A, c, pos, co, si);
-        rotate<V, PAIRS>(u, v, co, si);
+        turns<T, V>(A, c, pos, co, si);
+        Factors<V> f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) f.f0[i] = f.f2[i] = co[i], f.f1[i] = f.f3[i] = si[i];
+        rotate<V, PAIRS>(u, v, f);
       }
       store<T, V>(y + b, v);
     }
@@ -270,10 +352,13 @@ int launch(const Args& a, bool pairs, bool wide, cudaStream_t st) {
   const int64_t blocks = ceil_div(a.items * a.lanes, 256);
   if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
   const unsigned n = (unsigned)blocks;
+  const bool full = a.lanes * 2 * V == a.d;  // the chunks are 2 V coordinates each
   if (wide && pairs) norm_rope_wide_kernel<T, V, true><<<n, 256, 0, st>>>(a);
   else if (wide) norm_rope_wide_kernel<T, V, false><<<n, 256, 0, st>>>(a);
-  else if (pairs) norm_rope_kernel<T, V, true><<<n, 256, 0, st>>>(a);
-  else norm_rope_kernel<T, V, false><<<n, 256, 0, st>>>(a);
+  else if (pairs && full) norm_rope_kernel<T, V, true, true><<<n, 256, 0, st>>>(a);
+  else if (pairs) norm_rope_kernel<T, V, true, false><<<n, 256, 0, st>>>(a);
+  else if (full) norm_rope_kernel<T, V, false, true><<<n, 256, 0, st>>>(a);
+  else norm_rope_kernel<T, V, false, false><<<n, 256, 0, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -372,13 +457,14 @@ extern "C" tq_status tq_qk_norm_rope(const tq_rope* rope, tq_dtype dt, int64_t n
   const bool wide = chunks > 32;
   a.lanes = 1;
   while (a.lanes < 32 && a.lanes < chunks) a.lanes *= 2;
-  // as many heads a group as leave two groups for every place on the GPU (2048 threads per SM): the sines cost as
-  // much as two to three heads' memory time, and a call of few rows is over sooner with a head each
-  const int64_t heads = Hq + Hkv, places = (int64_t)tq::sm_count() * 2048 / a.lanes;
+  // as many heads a group as leave two groups for every place on the GPU (512 threads per SM): the heads share a
+  // token's sines, and a call of few rows is over sooner with a head each
+  const int64_t heads = Hq + Hkv, places = (int64_t)tq::sm_count() * 512 / a.lanes;
   a.hpg = wide ? 1 : (int)std::min<int64_t>(16, std::max<int64_t>(1, n_tok * heads / (2 * places)));
   a.blocks = (int)tq::ceil_div(heads, a.hpg);
   a.hpg = (int)tq::ceil_div(heads, a.blocks);  // even shares
   a.items = n_tok * a.blocks;
+  a.n_tok = n_tok;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   int e;
   if (dt == TQ_F32) e = v == 4 ? launch<float, 4>(a, pairs, wide, st) : launch<float, 1>(a, pairs, wide, st);
