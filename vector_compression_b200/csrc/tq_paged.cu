@@ -29,35 +29,60 @@ struct AppendArgs {
   int64_t n_tok;
   int B;
   const int32_t *cu, *start;
+  int per;    // tokens that a warp looks through for the first ones of runs
+  int parts;  // of a run
 };
 
-// Transposes a 32 x 32 bit matrix held one row per lane: afterwards bit t of
-// lane j's word is bit j of lane t's.
-__device__ __forceinline__ uint32_t transpose32(uint32_t w, int lane) {
+// Transposes 32 x 32 bit matrices held one row per lane: afterwards bit t of
+// lane j's word is bit j of lane t's.  The lanes with bit s swap their low parts
+// with the partners' high parts: for s = 16 and 8 whole bytes, a permute each,
+// then a rotation and a selection.
+struct Transpose {
+  uint32_t sel16, sel8, keep[3];
+  int rot[3];
+  __device__ __forceinline__ explicit Transpose(int lane) {
+    sel16 = lane & 16 ? 0x3276u : 0x5410u;
+    sel8 = lane & 8 ? 0x3715u : 0x6240u;
 #pragma unroll
-  for (int s = 16; s > 0; s >>= 1) {
-    // the lanes with bit s swap their low parts with the partners' high parts
-    const uint32_t m = s == 16 ? 0x0000ffffu : s == 8 ? 0x00ff00ffu : s == 4 ? 0x0f0f0f0fu : s == 2 ? 0x33333333u : 0x55555555u;
-    const uint32_t o = __shfl_xor_sync(0xffffffffu, w, s);
-    w = (lane & s) ? ((w & ~m) | ((o >> s) & m)) : ((w & m) | ((o << s) & ~m));
+    for (int i = 0; i < 3; ++i) {
+      const int s = 4 >> i;
+      const uint32_t m = s == 4 ? 0x0f0f0f0fu : s == 2 ? 0x33333333u : 0x55555555u;
+      keep[i] = lane & s ? ~m : m;
+      rot[i] = lane & s ? 32 - s : s;
+    }
   }
-  return w;
-}
+  __device__ __forceinline__ uint32_t operator()(uint32_t w) const {
+    w = __byte_perm(w, __shfl_xor_sync(0xffffffffu, w, 16), sel16);
+    w = __byte_perm(w, __shfl_xor_sync(0xffffffffu, w, 8), sel8);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      const uint32_t o = __shfl_xor_sync(0xffffffffu, w, 4 >> i);
+      w = (w & keep[i]) | (__funnelshift_l(o, o, rot[i]) & ~keep[i]);
+    }
+    return w;
+  }
+};
 
-// The sequence that token i belongs to, and its first and last+1 new token
-// (packed numbers); false when i belongs to none.  Called by a whole warp.
-__device__ __forceinline__ bool find_sequence(const AppendArgs& A, int64_t i, int lane, int& b, int64_t& t0, int64_t& t1) {
+// The sequence that token i belongs to, its first and last+1 new token (packed
+// numbers) and its start; false when i belongs to none.  Called by a whole warp.
+__device__ __forceinline__ bool find_sequence(const AppendArgs& A, int i, int lane, int& b, int& t0, int& t1, int& start) {
   int lo = 0, n = A.B;  // the last b with cu[b] <= i is in [lo, lo + n)
-  while (n > 1) {
+  while (n > 32) {
     const int step = (n + 31) / 32;
     const uint32_t le = __ballot_sync(0xffffffffu, lane * step < n && A.cu[lo + lane * step] <= i);
     const int last = le ? 31 - __clz((int)le) : 0;
     lo += last * step;
     n = min(step, n - last * step);
   }
-  b = lo;
-  t0 = A.cu[lo];
-  t1 = min64(A.cu[lo + 1], A.n_tok);
+  // of at most 32 each lane holds one: what is asked of the found one is there already
+  const int c0 = lane < n ? A.cu[lo + lane] : 0, c1 = lane < n ? A.cu[lo + lane + 1] : 0;
+  const int st = lane < n ? A.start[lo + lane] : 0;
+  const uint32_t le = __ballot_sync(0xffffffffu, lane < n && c0 <= i);
+  const int last = le ? 31 - __clz((int)le) : 0;
+  b = lo + last;
+  t0 = __shfl_sync(0xffffffffu, c0, last);
+  t1 = min(__shfl_sync(0xffffffffu, c1, last), (int)A.n_tok);
+  start = __shfl_sync(0xffffffffu, st, last);
   return t0 <= i && i < t1;
 }
 
@@ -73,115 +98,160 @@ __device__ __forceinline__ uint32_t place(const uint32_t (&p)[KV], int q) {
            (((n >> q) & m) << 3);
   }
   if (q == 2) return __funnelshift_l(p[2 % KV], p[2 % KV], 2);
-  const int s = 2 * q;
-  return ((p[0] >> s) & m) | (((p[1 % KV] >> s) & m) << 1) | (((p[0] >> (s + 1)) & m) << 2) |
-         (((p[1 % KV] >> (s + 1)) & m) << 3);
+  if (q == 0) return (p[0] & m) | ((p[1 % KV] & m) << 1) | ((p[0] & 2 * m) << 1) | ((p[1 % KV] & 2 * m) << 2);
+  return ((p[0] >> 2) & m) | ((p[1 % KV] >> 1) & 2 * m) | ((p[0] >> 1) & 4 * m) | (p[1 % KV] & 8 * m);
 }
 
-// A granule of G words from a ROW row to the record.
-template <int G>
-__device__ __forceinline__ void copy_granule(uint32_t* dst, const uint32_t* src) {
-  if (G == 4) *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(src);
-  else if (G == 2) *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(src);
-  else *dst = *src;
+// Where a run goes: the record of block `blk` of page `id` (as read from the table), null in a hole.
+__device__ __forceinline__ uint32_t* record_of(const AppendArgs& A, int32_t id, int blk_in_page, int h) {
+  if (id < 0 || id >= A.tab.n_pages) return nullptr;
+  return A.pool + id * A.L.page_words + ((int64_t)(A.layer * A.L.hkv + h) * A.L.nb + blk_in_page) * A.L.words;
 }
+
 template <int G>
-__device__ __forceinline__ void copy_keys(const AppendArgs& A, uint32_t* rec, int64_t row, int lane) {
+struct Granule {
+  using type = uint32_t;
+};
+template <>
+struct Granule<2> {
+  using type = uint2;
+};
+template <>
+struct Granule<4> {
+  using type = uint4;
+};
+
+// The key words of this lane's token, in granules of G words that lie in one of the two rows each.
+template <int G>
+__device__ __forceinline__ void write_keys(const AppendArgs& A, int32_t id, int blk_in_page, int h, int64_t row, int lane) {
+  using V = typename Granule<G>::type;
   const Layout& L = A.L;
   const uint32_t *c = A.kcodes + row * L.kw, *s = A.ksigns + row * L.sw;
-  if (L.kw % G == 0) {
-#pragma unroll 4
-    for (int p = 0; p < L.kw; p += G) copy_granule<G>(rec + (p * 32 + lane * G), c + p);
-#pragma unroll 4
-    for (int p = 0; p < L.sw; p += G) copy_granule<G>(rec + ((L.kw + p) * 32 + lane * G), s + p);
-  } else {
-    for (int w = 0; w < L.nk; ++w) rec[key_word_at(L, lane, w)] = w < L.kw ? c[w] : s[w - L.kw];
+  uint32_t* rec = nullptr;
+  for (int p0 = 0; p0 < L.nk; p0 += 4 * G) {
+    V v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int p = p0 + i * G;
+      if (p < L.nk) v[i] = *reinterpret_cast<const V*>(p < L.kw ? c + p : s + (p - L.kw));
+    }
+    if (!rec && !(rec = record_of(A, id, blk_in_page, h))) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (p0 + i * G < L.nk) *reinterpret_cast<V*>(rec + (p0 + i * G) * 32 + lane * G) = v[i];
   }
 }
+
+constexpr int kPartWords = 2;  // value words per plane (32 coordinates each) of a part
 
 // The new tokens that one 32-token block of one head gets (a run): tok .. tok +
 // len - 1 at places off ...; a lane is a token for the keys and a coordinate of
-// 32 for the values.
+// 32 for the values.  Part 0 is the keys and norms, part 1 + i some of the
+// coordinates' value words: warps of their own, a run's latency is theirs.  What
+// is written is read before the page's number is looked at, so that the two
+// latencies are one.
 template <int KV>
-__device__ __forceinline__ void write_run(const AppendArgs& A, uint32_t* rec, int h, int64_t tok, int off, int len, int lane) {
+__device__ __forceinline__ void write_run(const AppendArgs& A, int32_t id, int blk_in_page, int h, int tok, int off,
+                                          int len, int part, int lane) {
   const Layout& L = A.L;
   const bool mine = lane >= off && lane < off + len;
-  const int64_t row0 = tok * L.hkv + h, row = row0 + (int64_t)(lane - off) * L.hkv;
-  if (mine) {
-    if (L.gr == 4) copy_keys<4>(A, rec, row, lane);
-    else if (L.gr == 2) copy_keys<2>(A, rec, row, lane);
-    else copy_keys<1>(A, rec, row, lane);
-    rec[L.o_kn + lane] = __float_as_uint(A.knorms[row]);
-    rec[L.o_vn + lane] = __float_as_uint(A.vnorms[row]);
-    if (L.r16)
-      reinterpret_cast<uint16_t*>(rec + L.o_kr)[lane] = reinterpret_cast<const uint16_t*>(A.krnorms)[row];
-    else
-      rec[L.o_kr + lane] = __float_as_uint(A.krnorms[row]);
+  const int64_t row0 = (int64_t)tok * L.hkv + h, row = row0 + (lane - off) * L.hkv;
+  if (part == 0) {
+    if (!mine) return;
+    const float kn = A.knorms[row], vn = A.vnorms[row];
+    const uint32_t kr = L.r16 ? reinterpret_cast<const uint16_t*>(A.krnorms)[row] : __float_as_uint(A.krnorms[row]);
+    if (L.gr == 4 && L.kw % 4 == 0) write_keys<4>(A, id, blk_in_page, h, row, lane);
+    else if (L.gr == 2 && L.kw % 2 == 0) write_keys<2>(A, id, blk_in_page, h, row, lane);
+    uint32_t* rec = record_of(A, id, blk_in_page, h);
+    if (!rec) return;
+    if (L.kw % L.gr != 0 || L.gr == 1) {  // a granule with words of both rows
+      const uint32_t *c = A.kcodes + row * L.kw, *s = A.ksigns + row * L.sw;
+      for (int w = 0; w < L.nk; ++w) rec[key_word_at(L, lane, w)] = w < L.kw ? c[w] : s[w - L.kw];
+    }
+    rec[L.o_kn + lane] = __float_as_uint(kn);
+    rec[L.o_vn + lane] = __float_as_uint(vn);
+    if (L.r16) reinterpret_cast<uint16_t*>(rec + L.o_kr)[lane] = (uint16_t)kr;
+    else rec[L.o_kr + lane] = kr;
+    return;
   }
   const uint32_t own = (len == 32 ? 0xffffffffu : ((1u << len) - 1u)) << off;  // the run's tokens
-  const int wpp = L.dp / 32;
-  // the bits of the run's fields: the same placement of codes of ones
+  const int wpp = L.dp / 32, jw0 = (part - 1) * kPartWords;
+  // plane words of the part's coordinates: of a lane's token, or of a coordinate's few tokens
+  uint32_t p[kPartWords][KV];
+#pragma unroll
+  for (int j = 0; j < kPartWords; ++j)
+#pragma unroll
+    for (int q = 0; q < KV; ++q) p[j][q] = 0;
+  if (len <= 4) {  // below that many tokens picking their bits is shorter than the transposition of 32
+    for (int i = 0; i < len; ++i) {
+      const uint32_t* v = A.vcodes + (row0 + (int64_t)i * L.hkv) * (KV * wpp);
+#pragma unroll
+      for (int j = 0; j < kPartWords; ++j)
+#pragma unroll
+        for (int q = 0; q < KV; ++q)
+          if (jw0 + j < wpp) p[j][q] |= ((v[q * wpp + jw0 + j] >> lane) & 1u) << (off + i);
+    }
+  } else if (mine) {
+    const uint32_t* v = A.vcodes + row * (KV * wpp);
+#pragma unroll
+    for (int j = 0; j < kPartWords; ++j)
+#pragma unroll
+      for (int q = 0; q < KV; ++q)
+        if (jw0 + j < wpp) p[j][q] = v[q * wpp + jw0 + j];
+  }
+  uint32_t* rec = record_of(A, id, blk_in_page, h);
+  if (!rec) return;
+  const Transpose transpose(lane);
+  // the bits of the run's fields: the same placement of codes of ones (of four-bit codes a field's bits lie in one word)
   uint32_t ones[KV];
 #pragma unroll
   for (int q = 0; q < KV; ++q) ones[q] = own;
-#pragma unroll 4
-  for (int jw = 0; jw < wpp; ++jw) {
-    uint32_t* w = rec + L.o_v + 32 * jw + lane;
-    uint32_t old[KV], p[KV];
-    if (own != 0xffffffffu) {
 #pragma unroll
-      for (int q = 0; q < KV; ++q) old[q] = w[q * L.dp];
-    }
-    if (len <= 4) {  // below that many tokens picking their bits is shorter than the transposition of 32
+  for (int j = 0; j < kPartWords; ++j) {
+    if (jw0 + j >= wpp) break;
+    uint32_t* w = rec + L.o_v + 32 * (jw0 + j) + lane;
+    if (len > 4) {
 #pragma unroll
-      for (int q = 0; q < KV; ++q) p[q] = 0;
-      for (int i = 0; i < len; ++i) {
-#pragma unroll
-        for (int q = 0; q < KV; ++q)
-          p[q] |= ((A.vcodes[(row0 + (int64_t)i * L.hkv) * (KV * wpp) + q * wpp + jw] >> lane) & 1u) << (off + i);
-      }
-    } else {
-#pragma unroll
-      for (int q = 0; q < KV; ++q) p[q] = transpose32(mine ? A.vcodes[row * (KV * wpp) + q * wpp + jw] : 0u, lane);
+      for (int q = 0; q < KV; ++q) p[j][q] = transpose(p[j][q]);
     }
 #pragma unroll
     for (int q = 0; q < KV; ++q) {
-      // of four-bit codes a field's four bits lie in one word
-      const uint32_t msk = KV == 4 ? ((own >> q) & 0x11111111u) * 15u : place<KV>(ones, q);
-      const uint32_t v = place<KV>(p, q) & msk;
-      w[q * L.dp] = own == 0xffffffffu ? v : ((old[q] & ~msk) | v);
+      uint32_t v = place<KV>(p[j], q);
+      if (len < 32) {
+        const uint32_t msk = KV == 4 ? ((own >> q) & 0x11111111u) * 15u : place<KV>(ones, q);
+        v = (w[q * L.dp] & ~msk) | (v & msk);
+      }
+      w[q * L.dp] = v;
     }
   }
 }
 
-// Tokens that a warp looks through for the first ones of runs: the 32 of a
-// prompt's block then cost four warps' look, and a step's single tokens (cu ==
-// null, a token per warp) wait for no other.
-constexpr int kAppendTile = 8;
-
+// Block (4 tiles of tokens, head and part), a warp per tile.
 template <int KV>
-__global__ void __launch_bounds__(128) append_kernel(const AppendArgs A) {
+__global__ void __launch_bounds__(128, 6) append_kernel(const AppendArgs A) {
   const Layout& L = A.L;
   const int lane = threadIdx.x & 31;
-  const int64_t item = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  const int64_t tile = item / L.hkv;
-  const int h = (int)(item - tile * L.hkv);
-  const int per = A.cu ? kAppendTile : 1;
-  const int64_t end = min64(A.n_tok, (tile + 1) * per);
-  for (int64_t tok = tile * per; tok < end;) {
-    int b = (int)tok;
-    int64_t t0 = tok, t1 = tok + 1;
-    if (A.cu && !find_sequence(A, tok, lane, b, t0, t1)) {
-      ++tok;
+  const int h = blockIdx.y / A.parts, part = blockIdx.y - h * A.parts;
+  const int64_t first = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 5)) * A.per;
+  if (first >= A.n_tok) return;
+  const int end = (int)min64(A.n_tok, first + A.per);
+  int b = 0, t0 = 0, t1 = 0, start = 0;
+  for (int tok = (int)first; tok < end;) {
+    if (!A.cu) {
+      b = t0 = tok;
+      t1 = tok + 1;
+      start = A.start[b];
+    } else if (tok >= t1 && !find_sequence(A, tok, lane, b, t0, t1, start)) {
+      t1 = ++tok;
       continue;
     }
-    const int64_t pos = A.start[b] + (tok - t0);
-    const int off = (int)(pos & 31);
-    const int len = (int)min64(32 - off, t1 - tok);
+    const int64_t pos = (int64_t)start + tok - t0;
+    const int off = (int)pos & 31;
+    const int len = min(32 - off, t1 - tok);
     // a sequence's first new token begins a run, and so does every block's first
     if ((tok == t0 || off == 0) && pos >= 0 && pos < (int64_t)A.tab.max_pages * L.page) {
-      const int64_t at = record_at(L, A.tab, b, (int)(pos >> 5), A.layer, h);
-      if (at >= 0) write_run<KV>(A, A.pool + at, h, tok, off, len, lane);
+      const int blk = (int)(pos >> 5), pi = L.nb_shift >= 0 ? blk >> L.nb_shift : blk / L.nb;
+      write_run<KV>(A, A.tab.rows[b * A.tab.ld + pi], blk - pi * L.nb, h, tok, off, len, part, lane);
     }
     tok += len;
   }
@@ -279,6 +349,7 @@ __device__ __forceinline__ int32_t live_entry(const CompactArgs& A, int64_t b, i
 }
 
 __global__ void __launch_bounds__(256) mark_kernel(const CompactArgs A) {
+  let_next_start();
   const int64_t n = (int64_t)A.B * A.max_pages;
   for (int64_t e = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; e < n; e += (int64_t)gridDim.x * blockDim.x) {
     const int64_t b = e / A.max_pages;
@@ -293,6 +364,8 @@ __global__ void __launch_bounds__(256) mark_kernel(const CompactArgs A) {
 __global__ void __launch_bounds__(256) plan_kernel(const CompactArgs A) {
   __shared__ int s_sum[8][2];
   __shared__ int s_scan[8];
+  wait_for_previous();
+  let_next_start();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int words = (int)((A.n_pages + 31) / 32);
   const int w0 = blockIdx.x * 256;
@@ -355,11 +428,69 @@ __global__ void __launch_bounds__(256) plan_kernel(const CompactArgs A) {
   }
 }
 
+// mark and plan in one CTA, the bit map and its prefix sums in shared memory.
+__global__ void __launch_bounds__(1024) plan_small_kernel(const CompactArgs A) {
+  extern __shared__ uint32_t map[];  // [words] bits, then [words] used pages before a word
+  __shared__ int s_warp[32];
+  let_next_start();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int n_pages = (int)A.n_pages, words = (n_pages + 31) / 32;
+  int* pre = reinterpret_cast<int*>(map + words);
+  for (int w = tid; w < words; w += 1024) map[w] = 0;
+  __syncthreads();
+  const int n = A.B * A.max_pages;
+  for (int e = tid; e < n; e += 1024) {
+    const int b = e / A.max_pages;
+    const int32_t id = live_entry(A, b, e - b * A.max_pages);
+    if (id >= 0) atomicOr(&map[id >> 5], 1u << (id & 31));  // bits: the order does not matter
+  }
+  __syncthreads();
+  const int per = (words + 1023) / 1024, w0 = min(tid * per, words), w1 = min(w0 + per, words);
+  int own = 0;
+  for (int w = w0; w < w1; ++w) own += __popc(map[w]);
+  int upto = own;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += x;
+  }
+  if (lane == 31) s_warp[warp] = upto;
+  __syncthreads();
+  const int sums = s_warp[lane];
+  const int total = __reduce_add_sync(0xffffffffu, sums);
+  int before = __reduce_add_sync(0xffffffffu, lane < warp ? sums : 0) + upto - own;
+  for (int w = w0; w < w1; ++w) {
+    pre[w] = before;
+    before += __popc(map[w]);
+  }
+  __syncthreads();
+  // used pages below n_used, and so how many have to move
+  const int below = total >= n_pages ? total : pre[total >> 5] + __popc(map[total >> 5] & ((1u << (total & 31)) - 1u));
+  if (tid == 0) {
+    *A.n_used = total;
+    *A.moves = total - below;
+  }
+  for (int id = tid; id < n_pages; id += 1024) {
+    const uint32_t bits = map[id >> 5];
+    const int ahead = pre[id >> 5] + __popc(bits & ((1u << (id & 31)) - 1u));
+    const bool used = (bits >> (id & 31)) & 1u;
+    int r = -1;
+    if (used && id >= total) {
+      r = ahead - below;
+      A.from[r] = id;
+    } else if (!used && id < total) {
+      A.to[id - ahead] = id;
+    }
+    A.rank[id] = r;
+  }
+}
+
 // Moves the pages, in pieces of `piece` 16-byte words (a warp each), and
 // rewrites the tables.  Sources lie at and above n_used, destinations below it
 // on unused pages: no piece is read after another has written it.
 __global__ void __launch_bounds__(256) move_kernel(const CompactArgs A, int piece) {
   const int lane = threadIdx.x & 31;
+  wait_for_previous();
   const int64_t tid = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, threads = (int64_t)gridDim.x * blockDim.x;
   const int64_t n = (int64_t)A.B * A.max_pages;
   for (int64_t e = tid; e < n; e += threads) {
@@ -377,6 +508,9 @@ __global__ void __launch_bounds__(256) move_kernel(const CompactArgs A, int piec
               reinterpret_cast<const uint4*>(A.pool + A.from[m] * A.L.page_words) + at, min64(piece, quads - at), lane);
   }
 }
+
+// One CTA plans up to this many table entries and 32-page words of the map.
+constexpr int64_t kSmallEntries = 32768, kSmallWords = 4096;
 
 size_t round256(size_t b) { return (b + 255) & ~(size_t)255; }
 
@@ -451,16 +585,19 @@ extern "C" tq_status tq_paged_append(const tq_paged* pg, uint32_t* pool, int64_t
     return TQ_ERR_INVALID_ARG;
   if (!al16(kcodes) || !al16(ksigns) || !al16(knorms) || !al16(krnorms) || !al16(vcodes) || !al16(vnorms))
     return TQ_ERR_INVALID_ARG;
+  // A step's tokens are a run each, and wait for no other: a warp each.  Of prompts a warp looks through 32, in which
+  // one block begins; of shorter sequences through 8, of which several can begin a run.
+  const int per = !cu ? 1 : n_tok / B >= 64 ? 32 : 8;
+  const int parts = 1 + (L.dp / 32 + kPartWords - 1) / kPartWords;
   AppendArgs a = {L, {tables, table_ld, max_pages, n_pages}, pool, layer, kcodes, ksigns, vcodes, knorms, krnorms,
-                  vnorms, n_tok, B, cu, start};
-  const int64_t blocks = tq::ceil_div(tq::ceil_div(n_tok, cu ? kAppendTile : 1) * L.hkv, 4);
-  if (blocks > 0x7fffffffll) return TQ_ERR_UNSUPPORTED;
+                  vnorms, n_tok, B, cu, start, per, parts};
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const dim3 grid((unsigned)tq::ceil_div(tq::ceil_div(n_tok, per), 4), L.hkv * parts);
   switch (L.kv) {
-    case 1: append_kernel<1><<<(unsigned)blocks, 128, 0, st>>>(a); break;
-    case 2: append_kernel<2><<<(unsigned)blocks, 128, 0, st>>>(a); break;
-    case 3: append_kernel<3><<<(unsigned)blocks, 128, 0, st>>>(a); break;
-    default: append_kernel<4><<<(unsigned)blocks, 128, 0, st>>>(a); break;
+    case 1: append_kernel<1><<<grid, 128, 0, st>>>(a); break;
+    case 2: append_kernel<2><<<grid, 128, 0, st>>>(a); break;
+    case 3: append_kernel<3><<<grid, 128, 0, st>>>(a); break;
+    default: append_kernel<4><<<grid, 128, 0, st>>>(a); break;
   }
   return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
 }
@@ -509,12 +646,22 @@ extern "C" tq_status tq_paged_compact(const tq_paged* pg, uint32_t* pool, int64_
                    reinterpret_cast<int32_t*>(w + 256 + map + list), reinterpret_cast<int32_t*>(w + 256 + map + 2 * list),
                    reinterpret_cast<int32_t*>(w)};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (cudaMemsetAsync(a.used, 0, (size_t)(n_pages + 31) / 32 * 4, st) != cudaSuccess) return TQ_ERR_CUDA;
-  const int64_t entries = (int64_t)B * max_pages;
+  const int64_t entries = (int64_t)B * max_pages, words = (n_pages + 31) / 32;
   const int sms = tq::sm_count();
-  if (entries > 0)
-    mark_kernel<<<(unsigned)std::min<int64_t>(tq::ceil_div(entries, 256), (int64_t)sms * 8), 256, 0, st>>>(a);
-  plan_kernel<<<(unsigned)tq::ceil_div((n_pages + 31) / 32, 256), 256, 0, st>>>(a);
-  move_kernel<<<(unsigned)(sms * 8), 256, 0, st>>>(a, 512);
+  cudaError_t e = cudaSuccess;
+  if (entries <= kSmallEntries && words <= kSmallWords) {
+    plan_small_kernel<<<1, 1024, (size_t)words * 8, st>>>(a);
+  } else {
+    e = cudaMemsetAsync(a.used, 0, (size_t)words * 4, st);
+    if (e == cudaSuccess && entries > 0)
+      mark_kernel<<<(unsigned)std::min<int64_t>(tq::ceil_div(entries, 256), (int64_t)sms * 8), 256, 0, st>>>(a);
+    if (e == cudaSuccess) {
+      const dim3 plan((unsigned)tq::ceil_div(words, 256));
+      if (entries > 0) e = launch_after(plan_kernel, plan, 256, 0, st, a);
+      else plan_kernel<<<plan, 256, 0, st>>>(a);  // behind the memset
+    }
+  }
+  if (e == cudaSuccess) e = launch_after(move_kernel, dim3((unsigned)(sms * 8)), 256, 0, st, a, 512);
+  if (e != cudaSuccess) return TQ_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
 }

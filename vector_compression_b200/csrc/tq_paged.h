@@ -2,6 +2,8 @@
 // record's parts (include/tq.h, tq_paged_create).
 #pragma once
 
+#include <cuda_runtime.h>
+
 #include <cstdint>
 
 #include "tq_internal.h"
@@ -46,6 +48,26 @@ __device__ __forceinline__ int key_word_at(const Layout& L, int t, int w) {
 __device__ __forceinline__ int clamp_len(int len, const Layout& L, int max_pages) {
   const int top = max_pages * L.page;
   return len < 0 ? 0 : len > top ? top : len;
+}
+// Launches that depend on the one before them may be set up early: a kernel
+// waits here before it reads what that one wrote ...
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// ... and says here that its successor may be set up.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <typename... Ps, typename... As>
+cudaError_t launch_after(void (*kern)(Ps...), dim3 grid, int threads, size_t smem, cudaStream_t st, As... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at = {};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 #endif
 

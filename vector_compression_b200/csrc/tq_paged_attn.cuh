@@ -158,27 +158,6 @@ __device__ __forceinline__ void store_out(const AttnArgs& A, int64_t i, float v)
   else static_cast<__nv_bfloat16*>(A.out)[i] = __float2bfloat16_rn(v);
 }
 
-// Launches that depend on the one before them may be set up early: a kernel
-// waits here before it reads what that one wrote ...
-__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-// ... and says here that its successor may be set up.
-__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
-template <typename... Ps, typename... As>
-cudaError_t launch_after(void (*kern)(Ps...), dim3 grid, int threads, size_t smem, cudaStream_t st, As... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute at = {};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, args...);
-}
-
 // The tensor-core kernel (tq_paged_attn_tc.cuh): what it needs to know of a
 // shape, and its launch.  ctas == 0: not a shape of it.
 struct TcShape {
