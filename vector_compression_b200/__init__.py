@@ -8,7 +8,6 @@ patterns of the C ABI.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes as C
 from typing import Optional
 
@@ -28,9 +27,6 @@ __all__ = [
     "F32", "F16", "BF16", "LAYOUT_ROW", "LAYOUT_BLOCK32", "MODE_MSE", "MODE_PROD", "MODE_MSE_UNBIASED",
     "STORE_RNORM_F16", "ROT_HADAMARD", "ROT_DENSE", "ROPE_PLAIN", "ROPE_LINEAR", "ROPE_BANDS", "ROPE_YARN",
 ]
-
-
-_nothing = contextlib.nullcontext()
 
 
 def _torch():
@@ -362,13 +358,22 @@ def _call(name, device, stream, *args):
         stream = torch._C._cuda_getCurrentRawStream(i)
     else:
         stream = stream.cuda_stream
-    if torch.cuda.current_device() == i:
+    if torch._C._cuda_getDevice() == i:
         status = fn(*args, stream)
     else:
         with torch.cuda.device(i):
             status = fn(*args, stream)
     if status:
         L.check(name, status)
+
+
+def _empty(shape, dtype, device, stream):
+    """Memory of the stream that the call runs on, so that it is not given away while the call still uses it."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _one_device(*tensors):
@@ -412,13 +417,13 @@ def tq_qk_norm_rope(rope: Optional[TQRope], q, k, pos=None, wq=None, wk=None, ep
     dt = q.dtype
     device = _one_device(q, k, pos, wq, wk, q_out, k_out)
     if q_out is None:
-        q_out = torch.empty((n, Hq, d), dtype=dt, device=device)
+        q_out = _empty((n, Hq, d), dt, device, stream)
     qi, qo = _heads("q", q, n, Hq, d, dt), _heads("q_out", q_out, n, Hq, d, dt)
     Hkv, ki, ko = 0, (None, 0, 0), (None, 0, 0)
     if k is not None:
         Hkv = k.shape[1]
         if k_out is None:
-            k_out = torch.empty((n, Hkv, d), dtype=dt, device=device)
+            k_out = _empty((n, Hkv, d), dt, device, stream)
         ki, ko = _heads("k", k, n, Hkv, d, dt), _heads("k_out", k_out, n, Hkv, d, dt)
     if rope is not None and pos is None:
         raise ValueError("a rotation needs positions")
@@ -440,6 +445,7 @@ class TQPaged:
         self.kp, self.vp, self.layers, self.hkv, self.page = kp, vp, layers, hkv, page
         self.block_words, self.page_words = bw.value, pw.value
         self._rnorm = getattr(_torch(), kp.rnorm_dtype)
+        self._ws_bytes = {}  # of attention, by (sequences, query heads, device)
 
     @property
     def handle(self):
@@ -534,12 +540,15 @@ def tq_paged_attention(pg: TQPaged, q, pool, layer: int, lens, tables, scale: fl
         sb = Hq * d
     device = _one_device(q, pool, lens, tables, out, lse, ws)
     if out is None:
-        out = torch.empty((B, Hq, d), dtype=q.dtype, device=device)
+        out = _empty((B, Hq, d), q.dtype, device, stream)
     if lse is None and want_lse:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=device)
+        lse = _empty((B, Hq), torch.float32, device, stream)
     if ws is None:
-        with torch.cuda.device(device) if torch.cuda.current_device() != device.index else _nothing:
-            ws = _ws(tq_paged_attention_workspace_size(pg, B, Hq), device)
+        need = pg._ws_bytes.get((B, Hq, device.index))
+        if need is None:
+            with torch.cuda.device(device):
+                need = pg._ws_bytes[B, Hq, device.index] = tq_paged_attention_workspace_size(pg, B, Hq)
+        ws = _empty(need, torch.uint8, device, stream)
     _call("tq_paged_attention", device, stream, pg.handle, q.data_ptr(), _dtype_code(q), max(sb, Hq * d), B, Hq,
           *_pool(pg, pool), layer, _is("lens", lens, torch.int32, (B,)), *_table("tables", tables, B), scale,
           _is("out", out, q.dtype, (B, Hq, d)), None if lse is None else _is("lse", lse, torch.float32, (B, Hq)),
@@ -577,9 +586,9 @@ def tq_paged_compact(pg: TQPaged, pool, tables, lens, tables_out=None, n_used=No
     elif tables_out.shape != tables.shape or tables_out.stride() != tables.stride():
         raise ValueError("tables_out must have the shape and strides of tables")
     if n_used is None:
-        n_used = torch.empty(1, dtype=torch.int32, device=device)
+        n_used = _empty(1, torch.int32, device, stream)
     if ws is None:
-        ws = _ws(tq_paged_compact_workspace_size(pool.shape[0]), device)
+        ws = _empty(tq_paged_compact_workspace_size(pool.shape[0]), torch.uint8, device, stream)
     tab, ld, width = _table("tables", tables, B)
     _call("tq_paged_compact", device, stream, pg.handle, *_pool(pg, pool), tab,
           _table("tables_out", tables_out, B)[0], ld, width, _is("lens", lens, torch.int32, (B,)), B,

@@ -18,9 +18,7 @@ inline bool al256(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 255u
 
 // ---------------------------------------------------------------- queries
 
-// Largest entry in fixed point: the difference of two neighbouring place values,
-// at most 3/2 of it and a rounding, fits three signed bytes (127 2^16 and less).
-constexpr float kQMax = 5548000.0f;
+constexpr float kQMax = 8323072.0f;  // 127 2^16, the largest entry in fixed point: three signed bytes hold it
 
 // P_j of the tensor-core kernel's scores: x / 2^j as an integer.
 __device__ __forceinline__ int place_value(float x, int j) {
@@ -48,7 +46,6 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
 // not finite; the images are then 0).
 template <int A32>
 __device__ __forceinline__ void fixed_point(const float (&x)[A32], int n, float w, float k, int* p, float* c, int lane) {
-  const int in_byte = n == 64 ? 3 : 7;  // coordinate j is bit j & in_byte of its byte (or half byte)
   float mx = 1e-30f, bad = 0.f;
 #pragma unroll
   for (int a = 0; a < A32; ++a)
@@ -59,13 +56,13 @@ __device__ __forceinline__ void fixed_point(const float (&x)[A32], int n, float 
   mx = warp_max(mx);
   bad = warp_sum(bad);
   const float inv = bad == 0.f ? kQMax / mx : 0.f;
-  int sum = 0;  // |sum| < d_pad (kQMax + 2^6) < 2^31
+  int sum = 0;  // |sum| < d_pad (kQMax + 2^2) < 2^31
 #pragma unroll
   for (int a = 0; a < A32; ++a)
     if (32 * a < n) {
-      const int v = place_value(x[a] * inv, lane & in_byte);
+      const int v = place_value(x[a] * inv, lane & 3);  // coordinate j is bit j mod 4 of its half byte
       p[32 * a + lane] = v;
-      sum += v << (lane & in_byte);
+      sum += v << (lane & 3);
     }
   sum = __reduce_add_sync(0xffffffffu, sum);
   if (lane == 0) {
@@ -217,17 +214,13 @@ __global__ void __launch_bounds__(512) queries_kernel(const AttnArgs A, const QP
       if (slot < A.gh && head < A.G) {
         const bool which = step >= A32;
         const int n = which ? m : dp, st = which ? step - A32 : step;
-        // the product of k low bits of the bytes of the thread's word; in two-word planes two threads share one
-        const int top = n == 64 ? 4 : 8;
-        const int* p = (which ? reinterpret_cast<const int*>(us[head]) : pq[head]) +
-                       (n == 64 ? 32 * (tig & 1) + 4 * (tig >> 1) : 32 * (tig + (st & ~3)));
+        // bits of the thread's word, of both half bytes; in two-word planes two threads share one, a half byte each
+        const int j0 = n == 64 ? 32 * (tig & 1) + 4 * (tig >> 1) + 2 * st : 32 * (tig + (st & ~3)) + (st & 3);
+        const int* p = (which ? reinterpret_cast<const int*>(us[head]) : pq[head]) + j0;
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const int k = n == 64 ? 2 * st + 1 + r : (st & 3) + 1 + 4 * r;
+        for (int r = 0; r < 2; ++r)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            w[r] |= digit(p[8 * i + k - 1] - (k < top ? p[8 * i + k] : 0), piece) << (8 * i);
-        }
+          for (int i = 0; i < 4; ++i) w[r] |= digit(p[8 * i + (n == 64 ? r : 4 * r)], piece) << (8 * i);
       }
       reinterpret_cast<uint2*>(f0 + (int64_t)grp * A.frag_words)[(at - grp * steps) * NQ * 32 + t * 32 + lane] =
           make_uint2(w[0], w[1]);

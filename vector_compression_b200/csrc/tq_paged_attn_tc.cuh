@@ -10,14 +10,14 @@
 // alpha_S (2 b_S - 1) over the odd subsets S of the bits (b_S their XOR), the
 // contractions are against 0/1 bits: <q', b_S> per subset and <u, sigma>.  An
 // MMA's A rows are tokens, its K four bytes of the word that each of four
-// threads holds: x_k = word & (bytes of k low bits) is one instruction for four
-// of them, k = 1 .. 8 (the whole word), and sum_j b_j q_j = sum_k x_k (P_{k-1} -
-// P_k) with P_j = q_j / 2^j of the byte's bit j (P_8 = 0).  P is in fixed point,
-// an integer, so the differences are exact; three signed bytes hold them: hi
-// and mid of heads 4 nt .. 4 nt + 3 are tile nt (columns 2 h, 2 h + 1), lo of
-// all of them one more tile (columns 2 h, 2 h + 1: heads h and 4 + h), so that
-// thread column tig holds all of head tig (and 4 + tig).  The queries' images
-// are made once per call (queries_kernel).
+// threads holds: (word or word >> 4) & (0x01010101 << j) are four of its bits
+// with value 2^j, nine instructions for a word's 32.  The B operand carries
+// q' / 2^j in fixed point, three signed bytes: hi and mid of heads 4 nt ..
+// 4 nt + 3 are tile nt (columns 2 h, 2 h + 1), lo of all of them one more tile
+// (columns 2 h, 2 h + 1: heads h and 4 + h), so that thread column tig holds all
+// of head tig (and 4 + tig).  The queries' images are made once per call
+// (queries_kernel).  Seven masks of whole bytes (differences of q' / 2^j, j =
+// 0 .. 7) were 2% faster and 16 times coarser.
 //
 // Values.  The value words of a coordinate (tq_paged_create) turn into 3-bit
 // selectors of eight tokens with two to four bit operations, and byte permutes
@@ -26,9 +26,8 @@
 // tokens 4 i + s of the group's four blocks (thread column tig: block tig), B
 // the weights p ||v|| as two bytes (columns 2 h, 2 h + 1) relative to the
 // group's largest.  Products and sums are exact integers; the roundings are
-// those of q', u (2^-23 to 2^-16 of the largest entry by the bit's place in its
-// byte, 2^-18 on the average), the levels and the weights (2^-16 of the
-// largest), and fp32 outside.
+// those of q', u (2^-24 to 2^-21 of the largest entry by the bit's place), the
+// levels and the weights (2^-16 of the largest), and fp32 outside.
 #pragma once
 
 #include "tq_paged_attn.cuh"
@@ -106,14 +105,6 @@ template <int GR>
 __device__ __forceinline__ int word_place(int base, int wt) {
   if (GR == 4) return base / 4 * 128 + base % 4 + wt;
   return (base / 2 + wt / 2) * 64 + wt % 2;
-}
-
-// The low bits of a word's bytes that MMA step `st` takes (x of its first and second half of K): 1 .. 4 and
-// 5 .. 8 bits of whole words, or 1 .. 4 bits of the half of each byte where two threads share a word.
-template <bool SHARED>
-__device__ __forceinline__ constexpr uint32_t low_bits(int st, int second) {
-  const int k = SHARED ? 2 * st + 1 + second : st + 1 + 4 * second;
-  return 0x01010101u * ((1u << k) - 1u);
 }
 
 // Selectors (nibbles) of the eight tokens 4 i + s from a coordinate's value words.
@@ -294,7 +285,7 @@ __global__ void __launch_bounds__(64, Shape<KK, KV, NT, DP, MQ>::CTAS)
         constexpr int W4 = (WPP + 3) / 4;
 #pragma unroll
         for (int hf = 0; hf < W4; ++hf) {
-          uint32_t w1[FK + 1], w2[FK + 1];
+          uint32_t w1[FK + 1], w2[FK + 1], h1[FK + 1], h2[FK + 1];
 #pragma unroll
           for (int p = 0; p < KK; ++p) {
             const int base = word_place<S::GR>(p * WPP, wt) + hf * 128;  // hf > 0 only with granules of four
@@ -311,17 +302,23 @@ __global__ void __launch_bounds__(64, Shape<KK, KV, NT, DP, MQ>::CTAS)
             w2[FK] = kw[base + t2 * S::GR] >> ssh;
           }
 #pragma unroll
+          for (int f = 0; f <= FK; ++f) {
+            h1[f] = w1[f] >> 4;
+            h2[f] = w2[f] >> 4;
+          }
+#pragma unroll
           for (int st = 0; st < 4; ++st) {
 #pragma unroll
             for (int f = 0; f <= FK; ++f) {
               if (4 * hf + st >= (f < FK ? WPP : SW)) continue;
-              const bool shared_word = f < FK ? WPP == 2 : SW == 2;
-              const uint32_t ka = shared_word ? low_bits<true>(st, 0) : low_bits<false>(st, 0);
-              const uint32_t kb2 = shared_word ? low_bits<true>(st, 1) : low_bits<false>(st, 1);
+              // bit st of both half bytes, or, where two threads share a word and have one half byte each, two of it
+              const bool half = f < FK ? WPP == 2 : SW == 2;
+              const uint32_t ka = 0x01010101u << (half ? 2 * st % 4 : st), kc2 = half ? 2 * ka : ka;
               const int step = 4 * hf + st + (f < FK ? 0 : WPP);
 #pragma unroll
               for (int t = 0; t < NQ; ++t)
-                mma_us(acc[f][t], w1[f] & ka, w2[f] & ka, w1[f] & kb2, w2[f] & kb2, bq[step][t]);
+                mma_us(acc[f][t], w1[f] & ka, w2[f] & ka, (half ? w1[f] : h1[f]) & kc2, (half ? w2[f] : h2[f]) & kc2,
+                       bq[step][t]);
             }
           }
         }
