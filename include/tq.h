@@ -408,6 +408,9 @@ tq_status tq_qk_norm_rope(const tq_rope* rope, tq_dtype dt, int64_t n_tok, int d
  *   kp, vp  as tq_decode_attention (same d; Hadamard rotation, else
  *           TQ_ERR_UNSUPPORTED); both must outlive the handle
  *   layers 1..4096, Hkv 1..1024, page 32..65536
+ * tq_paged_attention reads kp's sketch: it runs on the device that was current
+ * when kp was created (TQ_ERR_INVALID_ARG on another); append, fork and compact
+ * on any.
  *
  * The pool is one caller-owned DEVICE array uint32 [n_pages][page_words],
  * 16-byte aligned, n_pages < 2^31; a page is [layers][Hkv][page / 32] block
@@ -427,7 +430,7 @@ tq_status tq_qk_norm_rope(const tq_rope* rope, tq_dtype dt, int64_t n_tok, int d
  *                            32 of word 2
  *                  k = 4     bits 4 i .. 4 i + 3 of word s: 0..7 for index 8 +
  *                            x, 8 + x for index 7 - x
- *   value norms  float [32]
+ *   value norms  float [32], not negative
  *
  * A page table is DEVICE int32 [B][table_ld >= max_pages]: entry i of row b is
  * the page of tokens [i page, (i + 1) page) of sequence b.  A page may stand
@@ -484,6 +487,11 @@ tq_status tq_paged_append(const tq_paged* pg, uint32_t* pool, int64_t n_pages, i
  *   ws      tq_paged_attention_workspace_size bytes, 256-byte aligned,
  *           nothing kept in it between calls: calls that overlap on the GPU
  *           need one each
+ * With key codes of 1..3 bits and (d_pad, m) of (64, 64), (128, 64), (128,
+ * 128) or (256, 256) the contractions are exact integer products on the
+ * tensor cores: the queries in fixed point (2^-21 of a head's largest entry),
+ * value levels and weights in 16 bits; other shapes take a slower kernel in
+ * fp32.
  */
 tq_status tq_paged_attention(const tq_paged* pg, const void* q, tq_dtype dt, int64_t q_ld, int B,
                              int Hq, const uint32_t* pool, int64_t n_pages, int layer,

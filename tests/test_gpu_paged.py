@@ -159,6 +159,11 @@ ATTENTION = [
     (128, 5, 3, 128, False, 1, 4, 32, [100]),
     (128, 3, 3, 128, False, 1, 16, 32, [140, 3]),
     (128, 3, 3, 512, False, 1, 9, 32, [64]),
+    (192, 3, 3, 256, False, 1, 6, 32, [129, 128]),
+    (64, 2, 2, 64, True, 2, 12, 32, [127, 200]),
+    (128, 2, 3, 64, False, 1, 11, 64, [256, 31]),
+    (256, 2, 1, 256, False, 1, 3, 32, [1, 161]),
+    (64, 4, 1, 64, False, 1, 5, 96, [97]),
 ]
 
 
@@ -242,6 +247,88 @@ def test_attention_extreme_scores_and_not_finite_queries():
     assert bool(torch.isnan(got[2, 1:3]).all()) and bool(torch.isnan(lse[2, 1:3]).all())
 
 
+def test_attention_more_sequences_than_a_warp_counts():
+    """Beyond 1024 sequences the shares come from the prefix sums, with empty sequences at both ends and between."""
+    kp, vp, kq, vq = quantizers(64, 3)
+    pg, model = tq.TQPaged(kp, vp, 1, 1, 32), Model(kp, vp, 1, 1, 32)
+    rng = np.random.default_rng(13)
+    lens = [int(x) for x in rng.integers(0, 9, 1400) * rng.integers(0, 2, 1400)]
+    lens[0] = lens[-1] = 0
+    lens[700] = 1500
+    pool, tables = random_cache(rng, model, lens, 48, 0)
+    q = torch.from_numpy(rng.standard_normal((1400, 2, 64))).to(DEV).half()
+    got, lse = tq.tq_paged_attention(pg, q, i32(pool), 0, ints(lens), ints(tables), 0.125, want_lse=True)
+    ref = model.attention(pool, 0, kq, vq, q.double().cpu().numpy(), lens, tables, 0.125)
+    check_attention(got, lse, ref, torch.float16)
+    tq.tq_sync_check()
+    none = tq.tq_paged_attention(pg, q, i32(pool), 0, torch.zeros(1400, dtype=torch.int32, device=DEV), ints(tables), 0.125)
+    assert bool((none == 0).all())
+
+
+def test_pages_beyond_32_bit_offsets():
+    """Everything that a small pool does, at the far end of one of more than 2^31 words, bit for bit."""
+    d, hkv, page = 128, 8, 64
+    kp, vp, _, _ = quantizers(d, 3)
+    pg = tq.TQPaged(kp, vp, 1, hkv, page)
+    far_pages = 2 ** 31 // pg.page_words + 40
+    far = torch.empty((far_pages, pg.page_words), dtype=torch.int32, device=DEV)
+    near = pg.new_pool(40)
+    g = torch.Generator(device=DEV).manual_seed(3)
+    lens, B = [200, 75], 2
+    x = torch.randn(sum(lens), hkv, d, device=DEV, generator=g).half()
+    keys, vals = tq.tq_encode_prod(kp, x), tq.tq_encode_mse(vp, x)
+    q = torch.randn(3, 4 * hkv, d, device=DEV, generator=g).half()
+    near_t = ints([[30, 3, 17, 9], [8, 21, -1, -1], [-1] * 4])
+    shift = far_pages - 40
+    far_t = torch.where(near_t >= 0, near_t + shift, near_t)
+    out = []
+    for pool, t, off in ((near, near_t, 0), (far, far_t, shift)):
+        n = ints(lens + [0])
+        tq.tq_paged_append(pg, pool, 0, keys, vals, ints([0, 0]), t[:2], cu=ints([0, 200, 275]))
+        tq.tq_paged_fork(pg, pool, t, n, ints([0]), ints([2]), ints([25 + off]))
+        a = tq.tq_paged_attention(pg, q, pool, 0, n, t, 0.09, want_lse=True)
+        n[1] = 0
+        b = tq.tq_paged_attention(pg, q, pool, 0, n, t, 0.09, want_lse=True)
+        used = tq.tq_paged_compact(pg, pool, t, n)
+        assert used.item() == 5 and int(t.max()) == 4
+        c = tq.tq_paged_attention(pg, q, pool, 0, n, t, 0.09, want_lse=True)
+        assert torch.equal(b[0], c[0]) and torch.equal(b[1], c[1])
+        out.append((*a, *b))
+    for u, v in zip(*out):
+        assert torch.equal(u, v)
+    tq.tq_sync_check()
+
+
+def test_calls_on_a_stream_that_is_not_current():
+    """Outputs and workspaces that a call makes belong to the stream it runs on."""
+    kp, vp, _, _ = quantizers(128, 3)
+    pg = tq.TQPaged(kp, vp, 1, 2, 32)
+    g = torch.Generator(device=DEV).manual_seed(4)
+    x = torch.randn(90, 2, 128, device=DEV, generator=g).half()
+    keys, vals = tq.tq_encode_prod(kp, x), tq.tq_encode_mse(vp, x)
+    t, n, q = ints([[4, 2, 0]]), ints([90]), torch.randn(1, 8, 128, device=DEV, generator=g).half()
+    pool = pg.new_pool(6)
+    tq.tq_paged_append(pg, pool, 0, keys, vals, ints([0]), t, cu=ints([0, 90]))
+    want = tq.tq_paged_attention(pg, q, pool, 0, n, t, 0.09, want_lse=True)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    other = pg.new_pool(6)
+    side.wait_stream(torch.cuda.current_stream())
+    tq.tq_paged_append(pg, other, 0, keys, vals, ints([0]), t, cu=ints([0, 90]), stream=side)
+    got = []
+    for _ in range(4):
+        got.append(tq.tq_paged_attention(pg, q, other, 0, n, t, 0.09, want_lse=True, stream=side))
+        torch.empty(1 << 22, dtype=torch.uint8, device=DEV).fill_(255)  # what the current stream takes meanwhile
+    t2 = t.clone()
+    side.wait_stream(torch.cuda.current_stream())
+    used = tq.tq_paged_compact(pg, other, t2, n, stream=side)
+    after = tq.tq_paged_attention(pg, q, other, 0, n, t2, 0.09, want_lse=True, stream=side)
+    side.synchronize()
+    assert used.item() == 3 and sorted(t2[0].tolist()) == [0, 1, 2]
+    for o, l in got + [after]:
+        assert torch.equal(o, want[0]) and torch.equal(l, want[1])
+
+
 def test_fork():
     kp, vp, _, _ = quantizers(64, 3)
     for page, layers in ((32, 1), (96, 3)):
@@ -295,7 +382,9 @@ def compact_model(pool, tables, lens, page):
     return np.where(ok, to[np.where(ok, tables, 0)], -1).astype(np.int32), n
 
 
-@pytest.mark.parametrize("n_pages,B,width", [(1, 1, 1), (31, 3, 5), (64, 8, 9), (1000, 40, 11), (20000, 300, 30)])
+# the last two: more pages, and more table entries, than one block plans
+@pytest.mark.parametrize("n_pages,B,width", [(1, 1, 1), (31, 3, 5), (64, 8, 9), (1000, 40, 11), (20000, 300, 30),
+                                             (140000, 50, 40), (900, 1100, 30)])
 def test_compact(n_pages, B, width):
     kp, vp, _, _ = quantizers(32, 2)
     page = 32

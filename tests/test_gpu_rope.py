@@ -114,6 +114,17 @@ def test_against_the_formula(case, dtype):
         assert ko is None
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("case", [
+    # so many rows that a group of lanes takes several heads, of both sides, the last groups fewer
+    (6001, 13, 6, 128, 128, False, True, "plain", True),
+    (9000, 9, 2, 96, 48, True, False, "bands", False),
+    (12345, 7, 0, 64, 64, False, True, "linear", True),
+])
+def test_many_rows(case, dtype):
+    test_against_the_formula(case, dtype)
+
+
 @pytest.mark.parametrize("pos", [0, 1, (1 << 20) - 1, 1 << 31, (1 << 40) + 12345, -1, -(1 << 33)])
 def test_far_and_negative_positions(pos):
     q = make(1, 2, 128, torch.float32, 7)

@@ -532,6 +532,7 @@ extern "C" tq_status tq_paged_create(const tq_params* kp, const tq_params* vp, i
   if (!pg) return TQ_ERR_INTERNAL;
   pg->kq = kp->q;
   pg->vq = vp->q;
+  pg->device = kp->device;
   tq::paged::Layout& L = pg->lay;
   L.kw = kp->q.code_words;
   L.sw = kp->q.sign_words;

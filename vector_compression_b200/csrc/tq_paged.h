@@ -87,5 +87,6 @@ inline bool mis4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) !
 
 struct tq_paged {
   tq::QParams kq, vq;
+  int device;  // of kq's sketch
   tq::paged::Layout lay;
 };

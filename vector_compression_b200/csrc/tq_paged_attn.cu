@@ -527,6 +527,8 @@ extern "C" tq_status tq_paged_attention(const tq_paged* pg, const void* q, tq_dt
   const tq_status s = tq_paged_attention_workspace_size(pg, B, Hq, &need);
   if (s != TQ_OK) return s;
   const Layout& L = pg->lay;
+  int device = 0;
+  if (cudaGetDevice(&device) != cudaSuccess || device != pg->device) return TQ_ERR_INVALID_ARG;
   if ((dt != TQ_F32 && dt != TQ_F16 && dt != TQ_BF16) || layer < 0 || layer >= L.layers) return TQ_ERR_INVALID_ARG;
   if (B == 0) return TQ_OK;
   if (bad_pool(L, pool, n_pages) || bad_table(L, tables, table_ld, max_pages)) return TQ_ERR_INVALID_ARG;
