@@ -53,9 +53,14 @@ def _ptr(t) -> C.c_void_p:
     return C.c_void_p(0 if t is None else t.data_ptr())
 
 
+_dtype_codes = {}
+
+
 def _dtype_code(t) -> int:
-    torch = _torch()
-    return {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}[t.dtype]
+    if not _dtype_codes:
+        torch = _torch()
+        _dtype_codes.update({torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16})
+    return _dtype_codes[t.dtype]
 
 
 def _ws(nbytes: int, device):
@@ -335,6 +340,8 @@ class TQRope:
 
     @property
     def handle(self):
+        if not self._h:
+            raise ValueError("a closed TQRope")  # a null handle means no rotation
         return self._h
 
     def close(self):
@@ -374,6 +381,13 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _empty_as(x, device, stream):
+    """Contiguous memory of x's shape and type."""
+    if stream is None and x.is_contiguous():
+        return _torch().empty_like(x)  # the shortest way
+    return _empty(x.shape, x.dtype, device, stream)
 
 
 def _one_device(*tensors):
@@ -416,15 +430,21 @@ def tq_qk_norm_rope(rope: Optional[TQRope], q, k, pos=None, wq=None, wk=None, ep
     n, Hq, d = q.shape
     dt = q.dtype
     device = _one_device(q, k, pos, wq, wk, q_out, k_out)
+    qi = _heads("q", q, n, Hq, d, dt)
     if q_out is None:
-        q_out = _empty((n, Hq, d), dt, device, stream)
-    qi, qo = _heads("q", q, n, Hq, d, dt), _heads("q_out", q_out, n, Hq, d, dt)
+        q_out = _empty_as(q, device, stream)
+        qo = q_out.data_ptr(), Hq * d, d
+    else:
+        qo = _heads("q_out", q_out, n, Hq, d, dt)
     Hkv, ki, ko = 0, (None, 0, 0), (None, 0, 0)
     if k is not None:
         Hkv = k.shape[1]
+        ki = _heads("k", k, n, Hkv, d, dt)
         if k_out is None:
-            k_out = _empty((n, Hkv, d), dt, device, stream)
-        ki, ko = _heads("k", k, n, Hkv, d, dt), _heads("k_out", k_out, n, Hkv, d, dt)
+            k_out = _empty_as(k, device, stream)
+            ko = k_out.data_ptr(), Hkv * d, d
+        else:
+            ko = _heads("k_out", k_out, n, Hkv, d, dt)
     if rope is not None and pos is None:
         raise ValueError("a rotation needs positions")
     _call("tq_qk_norm_rope", device, stream, None if rope is None else rope.handle, _dtype_code(q), n, d, Hq, *qi,
@@ -445,7 +465,7 @@ class TQPaged:
         self.kp, self.vp, self.layers, self.hkv, self.page = kp, vp, layers, hkv, page
         self.block_words, self.page_words = bw.value, pw.value
         self._rnorm = getattr(_torch(), kp.rnorm_dtype)
-        self._ws_bytes = {}  # of attention, by (sequences, query heads, device)
+        self._ws_bytes = {}  # of attention by (sequences, query heads, device), of compaction by pages
 
     @property
     def handle(self):
@@ -540,7 +560,7 @@ def tq_paged_attention(pg: TQPaged, q, pool, layer: int, lens, tables, scale: fl
         sb = Hq * d
     device = _one_device(q, pool, lens, tables, out, lse, ws)
     if out is None:
-        out = _empty((B, Hq, d), q.dtype, device, stream)
+        out = _empty_as(q, device, stream)
     if lse is None and want_lse:
         lse = _empty((B, Hq), torch.float32, device, stream)
     if ws is None:
@@ -588,11 +608,15 @@ def tq_paged_compact(pg: TQPaged, pool, tables, lens, tables_out=None, n_used=No
     if n_used is None:
         n_used = _empty(1, torch.int32, device, stream)
     if ws is None:
-        ws = _empty(tq_paged_compact_workspace_size(pool.shape[0]), torch.uint8, device, stream)
+        need = pg._ws_bytes.get(pool.shape[0])
+        if need is None:
+            need = pg._ws_bytes[pool.shape[0]] = tq_paged_compact_workspace_size(pool.shape[0])
+        ws = _empty(need, torch.uint8, device, stream)
     tab, ld, width = _table("tables", tables, B)
-    _call("tq_paged_compact", device, stream, pg.handle, *_pool(pg, pool), tab,
-          _table("tables_out", tables_out, B)[0], ld, width, _is("lens", lens, torch.int32, (B,)), B,
-          _is("n_used", n_used, torch.int32, (1,)), ws.data_ptr(), ws.numel() * ws.element_size())
+    out = tab if tables_out is tables else _table("tables_out", tables_out, B)[0]
+    _call("tq_paged_compact", device, stream, pg.handle, *_pool(pg, pool), tab, out, ld, width,
+          _is("lens", lens, torch.int32, (B,)), B, _is("n_used", n_used, torch.int32, (1,)), ws.data_ptr(),
+          ws.numel() * ws.element_size())
     return n_used
 
 
