@@ -484,8 +484,8 @@ tq_status tq_paged_append(const tq_paged* pg, uint32_t* pool, int64_t n_pages, i
  *   lse     DEVICE float [B][Hq] or NULL: log(sum(exp(scale * s))), -inf
  *           where there is no token; joins the result with attention over
  *           tokens that are not in the cache
- *   ws      tq_paged_attention_workspace_size bytes, 256-byte aligned,
- *           nothing kept in it between calls: calls that overlap on the GPU
+ *   ws      tq_paged_attention_workspace_size bytes (for the current device),
+ *           256-byte aligned, nothing kept in it between calls: calls that overlap on the GPU
  *           need one each
  * With key codes of 1..3 bits and (d_pad, m) of (64, 64), (128, 64), (128,
  * 128) or (256, 256) the contractions are exact integer products on the

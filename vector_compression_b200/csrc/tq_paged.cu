@@ -102,10 +102,10 @@ __device__ __forceinline__ uint32_t place(const uint32_t (&p)[KV], int q) {
   return ((p[0] >> 2) & m) | ((p[1 % KV] >> 1) & 2 * m) | ((p[0] >> 1) & 4 * m) | (p[1 % KV] & 8 * m);
 }
 
-// Where a run goes: the record of block `blk` of page `id` (as read from the table), null in a hole.
-__device__ __forceinline__ uint32_t* record_of(const AppendArgs& A, int32_t id, int blk_in_page, int h) {
-  if (id < 0 || id >= A.tab.n_pages) return nullptr;
-  return A.pool + id * A.L.page_words + ((int64_t)(A.layer * A.L.hkv + h) * A.L.nb + blk_in_page) * A.L.words;
+// Where a run goes: the record of its block, given the page as read from the table; null in a hole.
+__device__ __forceinline__ uint32_t* record_of(const AppendArgs& A, int32_t page, int blk, int h) {
+  const int64_t at = record_in(A.L, A.tab, page, blk, A.layer, h);
+  return at < 0 ? nullptr : A.pool + at;
 }
 
 template <int G>
@@ -123,7 +123,7 @@ struct Granule<4> {
 
 // The key words of this lane's token, in granules of G words that lie in one of the two rows each.
 template <int G>
-__device__ __forceinline__ void write_keys(const AppendArgs& A, int32_t id, int blk_in_page, int h, int64_t row, int lane) {
+__device__ __forceinline__ void write_keys(const AppendArgs& A, int32_t page, int blk, int h, int64_t row, int lane) {
   using V = typename Granule<G>::type;
   const Layout& L = A.L;
   const uint32_t *c = A.kcodes + row * L.kw, *s = A.ksigns + row * L.sw;
@@ -135,7 +135,7 @@ __device__ __forceinline__ void write_keys(const AppendArgs& A, int32_t id, int 
       const int p = p0 + i * G;
       if (p < L.nk) v[i] = *reinterpret_cast<const V*>(p < L.kw ? c + p : s + (p - L.kw));
     }
-    if (!rec && !(rec = record_of(A, id, blk_in_page, h))) return;
+    if (!rec && !(rec = record_of(A, page, blk, h))) return;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (p0 + i * G < L.nk) *reinterpret_cast<V*>(rec + (p0 + i * G) * 32 + lane * G) = v[i];
@@ -151,7 +151,7 @@ constexpr int kPartWords = 2;  // value words per plane (32 coordinates each) of
 // is written is read before the page's number is looked at, so that the two
 // latencies are one.
 template <int KV>
-__device__ __forceinline__ void write_run(const AppendArgs& A, int32_t id, int blk_in_page, int h, int tok, int off,
+__device__ __forceinline__ void write_run(const AppendArgs& A, int32_t page, int blk, int h, int tok, int off,
                                           int len, int part, int lane) {
   const Layout& L = A.L;
   const bool mine = lane >= off && lane < off + len;
@@ -160,9 +160,9 @@ __device__ __forceinline__ void write_run(const AppendArgs& A, int32_t id, int b
     if (!mine) return;
     const float kn = A.knorms[row], vn = A.vnorms[row];
     const uint32_t kr = L.r16 ? reinterpret_cast<const uint16_t*>(A.krnorms)[row] : __float_as_uint(A.krnorms[row]);
-    if (L.gr == 4 && L.kw % 4 == 0) write_keys<4>(A, id, blk_in_page, h, row, lane);
-    else if (L.gr == 2 && L.kw % 2 == 0) write_keys<2>(A, id, blk_in_page, h, row, lane);
-    uint32_t* rec = record_of(A, id, blk_in_page, h);
+    if (L.gr == 4 && L.kw % 4 == 0) write_keys<4>(A, page, blk, h, row, lane);
+    else if (L.gr == 2 && L.kw % 2 == 0) write_keys<2>(A, page, blk, h, row, lane);
+    uint32_t* rec = record_of(A, page, blk, h);
     if (!rec) return;
     if (L.kw % L.gr != 0 || L.gr == 1) {  // a granule with words of both rows
       const uint32_t *c = A.kcodes + row * L.kw, *s = A.ksigns + row * L.sw;
@@ -199,7 +199,7 @@ __device__ __forceinline__ void write_run(const AppendArgs& A, int32_t id, int b
       for (int q = 0; q < KV; ++q)
         if (jw0 + j < wpp) p[j][q] = v[q * wpp + jw0 + j];
   }
-  uint32_t* rec = record_of(A, id, blk_in_page, h);
+  uint32_t* rec = record_of(A, page, blk, h);
   if (!rec) return;
   const Transpose transpose(lane);
   // the bits of the run's fields: the same placement of codes of ones (of four-bit codes a field's bits lie in one word)
@@ -250,8 +250,8 @@ __global__ void __launch_bounds__(128, 6) append_kernel(const AppendArgs A) {
     const int len = min(32 - off, t1 - tok);
     // a sequence's first new token begins a run, and so does every block's first
     if ((tok == t0 || off == 0) && pos >= 0 && pos < (int64_t)A.tab.max_pages * L.page) {
-      const int blk = (int)(pos >> 5), pi = L.nb_shift >= 0 ? blk >> L.nb_shift : blk / L.nb;
-      write_run<KV>(A, A.tab.rows[b * A.tab.ld + pi], blk - pi * L.nb, h, tok, off, len, part, lane);
+      const int blk = (int)(pos >> 5);
+      write_run<KV>(A, page_entry(L, A.tab, b, blk), blk, h, tok, off, len, part, lane);
     }
     tok += len;
   }

@@ -34,13 +34,19 @@ struct Table {
 };
 
 #ifdef __CUDACC__
-// First word of the record of block `blk` (32 tokens) of a sequence in layer
-// `layer`, head h; -1 in a hole.  64-bit: a pool can be larger than 2^31 words.
+// The page of block `blk` (32 tokens) of a sequence, as its table row says.
+__device__ __forceinline__ int page_of(const Layout& L, int blk) { return L.nb_shift >= 0 ? blk >> L.nb_shift : blk / L.nb; }
+__device__ __forceinline__ int32_t page_entry(const Layout& L, const Table& t, int64_t b, int blk) {
+  return t.rows[b * t.ld + page_of(L, blk)];
+}
+// First word of the record of block `blk` in layer `layer`, head h, given its
+// page; -1 in a hole.  64-bit: a pool can be larger than 2^31 words.
+__device__ __forceinline__ int64_t record_in(const Layout& L, const Table& t, int32_t page, int blk, int layer, int h) {
+  if (page < 0 || page >= t.n_pages) return -1;
+  return page * L.page_words + ((int64_t)(layer * L.hkv + h) * L.nb + (blk - page_of(L, blk) * L.nb)) * L.words;
+}
 __device__ __forceinline__ int64_t record_at(const Layout& L, const Table& t, int64_t b, int blk, int layer, int h) {
-  const int pi = L.nb_shift >= 0 ? blk >> L.nb_shift : blk / L.nb;
-  const int32_t id = t.rows[b * t.ld + pi];
-  if (id < 0 || id >= t.n_pages) return -1;
-  return id * L.page_words + ((int64_t)(layer * L.hkv + h) * L.nb + (blk - pi * L.nb)) * L.words;
+  return record_in(L, t, page_entry(L, t, b, blk), blk, layer, h);
 }
 __device__ __forceinline__ int key_word_at(const Layout& L, int t, int w) {
   return (w / L.gr) * (32 * L.gr) + t * L.gr + w % L.gr;

@@ -60,7 +60,7 @@ __device__ __forceinline__ int worker_of(const AttnArgs& A, int64_t units, int64
 }
 
 __device__ __forceinline__ int units_of(const AttnArgs& A, int64_t b) {
-  return (clamp_len(A.lens[b], A.L, A.tab.max_pages) + 32 * kUnit - 1) / (32 * kUnit);
+  return (int)(((unsigned)clamp_len(A.lens[b], A.L, A.tab.max_pages) + 32u * kUnit - 1u) / (32u * kUnit));
 }
 
 struct Segment {
@@ -97,14 +97,15 @@ __device__ __forceinline__ Segment segment_at(const AttnArgs& A, int64_t u0, int
   return segment_in(A, lo, (int)(A.prefix[lo + 1] - p), u0 - A.hv * p, u1 - u0);
 }
 
-// The segment behind s, for a share that goes on from unit u0 to u1.
-__device__ __forceinline__ Segment segment_after(const AttnArgs& A, const Segment& s, int64_t u0, int64_t u1) {
-  int b = s.b, n = units_of(A, b);
+// The segment behind s, for a share that goes on from unit u0 to u1; n1: the units a head of the sequence behind it,
+// read beforehand.
+__device__ __forceinline__ Segment segment_after(const AttnArgs& A, const Segment& s, int n1, int64_t u0, int64_t u1) {
+  int b = s.b, n = (int)(((unsigned)s.len + 32u * kUnit - 1u) / (32u * kUnit));
   int64_t rel = (int64_t)(s.h + 1) * n;
   if (s.h + 1 == A.hv) {
     rel = 0;
-    do n = units_of(A, ++b);
-    while (n == 0);  // ends: a unit u0 < u1 <= units is some sequence's
+    ++b;
+    for (n = n1; n == 0;) n = units_of(A, ++b);  // ends: a unit u0 < u1 <= units is some sequence's
   }
   return segment_in(A, b, n, rel, u1 - u0);
 }

@@ -2,9 +2,9 @@
 // for d_pad 64, 128 and 256 (tq_paged_attn.cuh: the split of the work).
 //
 // A warp is a worker: it takes its share of 32-token block records four at a
-// time (a unit, here a group), keys and values each staged by bulk copies; the next group's
-// keys load while this one's values are summed, its values while the next keys
-// are scored.  No warp waits for another.
+// time (a unit, here a group), keys and values each staged by bulk copies; the
+// next group's keys load while this one's values are summed, its values while
+// the next keys are scored.  No warp waits for another.
 //
 // Scores.  With the codebook an odd function of its index bits, C[idx] = sum_S
 // alpha_S (2 b_S - 1) over the odd subsets S of the bits (b_S their XOR), the
@@ -28,6 +28,11 @@
 // group's largest.  Products and sums are exact integers; the roundings are
 // those of q', u (2^-24 to 2^-21 of the largest entry by the bit's place), the
 // levels and the weights (2^-16 of the largest), and fp32 outside.
+//
+// What bounds it (8 sequences of 31 thousand tokens, 8 KV heads of 4 query
+// heads, d = m = 128, 3 bits: 78 us, 2.7 TB/s, of 33 us that the bytes take): the
+// ALU (51% busy: masks, permutes) and the tensor pipe (39%), which overlap only
+// in part; with 4, 8 and 12 warps an SM it takes 104, 80 and 78 us.
 #pragma once
 
 #include "tq_paged_attn.cuh"
@@ -51,13 +56,14 @@ struct Shape {
   static constexpr int XW = 4 * 32 * 4 * NT;
   static_assert(XW >= 8 * NT * WC, "the weights fit the scores' place");
   // the running sums: in shared memory the loop over coordinates need not be unrolled (a fourth of the code, which a
-  // short call fetches for one use) and 16 registers a tile are free; at d_pad 256 two warps an SM would not fit
+  // short call fetches for one use) and 16 registers a tile are free; at d_pad 256 two warps of an SM's eight would not fit
   static constexpr bool O_SMEM = DP < 256;
   static constexpr int OW = O_SMEM ? DP / 32 * 32 * 4 * NT : 0;
   static constexpr int WARP_BYTES = 4 * (4 * KB + 4 * VB + XW + OW) + 16;
   static constexpr int WARPS = 2;
   static constexpr int SMEM = WARPS * WARP_BYTES;
-  // resident CTAs: the shared memory's limit, and the registers'
+  // resident CTAs: the shared memory's limit, and the registers'.  Two tiles of heads at five CTAs (168 registers, ten
+  // warps on four schedulers) took 81 us where four take 69 (8 sequences of 31 thousand tokens, 4 KV heads of 8)
   static constexpr int BY_SMEM = 233472 / (SMEM + 1024);
   static constexpr int BY_REGS = DP == 64 ? 8 : DP == 128 ? (NT == 1 ? 6 : 4) : 4;
   static constexpr int CTAS = BY_SMEM < BY_REGS ? BY_SMEM : BY_REGS;
@@ -177,14 +183,14 @@ __global__ void __launch_bounds__(64, Shape<KK, KV, NT, DP, MQ>::CTAS)
   // lane i < 4 knows of block i of the group at sg.blk: its record (-1: none) and its tokens
   int64_t at = -1;
   int nt = 0;
-  auto describe = [&](const Segment& s, int64_t& a, int& n) {
-    a = -1;
-    n = 0;
+  // the table is read long before its entry is looked at
+  auto entry = [&](const Segment& s) -> int32_t {
+    return lane < kUnit && s.blk + lane < s.end ? page_entry(A.L, A.tab, s.b, s.blk + lane) : -1;
+  };
+  auto describe = [&](const Segment& s, int32_t page, int64_t& a, int& n) {
     const int blk = s.blk + lane;
-    if (lane < 4 && blk < s.end) {
-      a = record_at(A.L, A.tab, s.b, blk, A.layer, s.kvh);
-      if (a >= 0) n = min(32, s.len - 32 * blk);
-    }
+    a = record_in(A.L, A.tab, page, blk, A.layer, s.kvh);
+    n = a >= 0 ? min(32, s.len - 32 * blk) : 0;
   };
   auto stage = [&](int64_t a, bool keys) {
     const uint32_t there = __ballot_sync(0xffffffffu, a >= 0);
@@ -194,7 +200,7 @@ __global__ void __launch_bounds__(64, Shape<KK, KV, NT, DP, MQ>::CTAS)
     if (a >= 0)
       bulk_copy(smem_at(keys ? kb + lane * S::KB : vb + lane * S::VB), A.pool + a + (keys ? 0 : A.L.o_v), bytes, bar);
   };
-  describe(sg, at, nt);
+  describe(sg, entry(sg), at, nt);
   stage(at, true);
   stage(at, false);
 
@@ -248,6 +254,7 @@ __global__ void __launch_bounds__(64, Shape<KK, KV, NT, DP, MQ>::CTAS)
   };
   start_sums();
 
+  int units_behind = units_of(A, min(sg.b + 1, A.B - 1));  // a head of the next sequence, read a segment ahead
   bool ok = true;
   uint32_t phase = 0, k_phase = 0;  // of this group, and of the keys staged last
   for (;; phase ^= 1u) {
@@ -256,10 +263,8 @@ __global__ void __launch_bounds__(64, Shape<KK, KV, NT, DP, MQ>::CTAS)
     ++u;
     nx.blk += kUnit;
     const bool last = nx.blk >= sg.end, done = u >= u_end;
-    if (last && !done) nx = segment_after(A, sg, u, u_end);
-    int64_t nat = -1;
-    int nnt = 0;
-    if (!done) describe(nx, nat, nnt);
+    if (last && !done) nx = segment_after(A, sg, units_behind, u, u_end);
+    const int32_t page = done ? -1 : entry(nx);
 
     // ---------------- scores, as powers of two
     if (!(ok = __all_sync(0xffffffffu, bounded_wait<true>(bar_k, phase, A.err)))) break;
@@ -356,7 +361,10 @@ __global__ void __launch_bounds__(64, Shape<KK, KV, NT, DP, MQ>::CTAS)
       for (int n = 0; n < NT; ++n) xs[(i * NT + n) * 32] = make_float4(x[n][0], x[n][1], x[n][2], x[n][3]);
     }
     __syncwarp();  // the keys have been read
+    int64_t nat = -1;
+    int nnt = 0;
     if (!done) {
+      describe(nx, page, nat, nnt);
       stage(nat, true);
       k_phase ^= 1u;
     }
@@ -520,7 +528,10 @@ __global__ void __launch_bounds__(64, Shape<KK, KV, NT, DP, MQ>::CTAS)
         }
       }
       start_sums();
-      if (!done) queries(nx);
+      if (!done) {
+        queries(nx);
+        units_behind = units_of(A, min(nx.b + 1, A.B - 1));
+      }
     }
     if (done) break;
     sg = nx;
