@@ -86,6 +86,10 @@ def test_the_binding_wants_cuda_tensors():
     q, pos = torch.zeros(2, 4, 64), torch.zeros(2, dtype=torch.int64)
     with pytest.raises(ValueError):
         tq.tq_qk_norm_rope(tq.TQRope(64), q, None, pos)
+    with pytest.raises(ValueError):
+        tq.tq_qk_norm_rope(tq.TQRope(64), q[0], None, pos)
+    with pytest.raises(ValueError):
+        tq.tq_qk_norm_rope(tq.TQRope(64), q.double(), None, pos)
 
 
 def test_a_closed_rotation_is_not_no_rotation():

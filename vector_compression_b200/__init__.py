@@ -356,68 +356,27 @@ class TQRope:
             pass
 
 
-def _call(name, device, stream, *args):
-    """Call an entry point with the device current and the stream last; raises on a bad status."""
-    torch = _torch()
-    fn = getattr(L.lib(), name)
-    i = device.index
-    if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(i)
-    else:
-        stream = stream.cuda_stream
-    if torch._C._cuda_getDevice() == i:
-        status = fn(*args, stream)
-    else:
-        with torch.cuda.device(i):
-            status = fn(*args, stream)
-    if status:
-        L.check(name, status)
+_binding = None
 
 
-def _empty(shape, dtype, device, stream):
-    """Memory of the stream that the call runs on, so that it is not given away while the call still uses it."""
-    torch = _torch()
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+def _bound():
+    """The calls on tensors (csrc/binding/tq_torch.cpp); loads libtq.so with it."""
+    global _binding
+    if _binding is None:
+        L.lib()
+        _torch()
+        from . import _torch_binding
+        _binding = _torch_binding
+    return _binding
 
 
-def _empty_as(x, device, stream):
-    """Contiguous memory of x's shape and type."""
-    if stream is None and x.is_contiguous():
-        return _torch().empty_like(x)  # the shortest way
-    return _empty(x.shape, x.dtype, device, stream)
-
-
-def _one_device(*tensors):
-    """The CUDA device that every given tensor is on."""
-    at = -2
-    for t in tensors:
-        if t is not None:
-            i = t.get_device()
-            if i != at and at != -2:
-                raise ValueError("the tensors are on different devices")
-            at = i
-    if at < 0:
-        raise ValueError("a CUDA device is needed")
-    return tensors[0].device
-
-
-def _is(name, t, dtype, shape):
-    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous {dtype} {tuple(shape)}")
-    return t.data_ptr()
-
-
-def _heads(name, x, n, heads, d, dtype):
-    """Pointer, token and head strides of a [n, heads, d] tensor whose last dimension is contiguous."""
-    if x.dtype != dtype or x.shape != (n, heads, d):
-        raise ValueError(f"{name} must be [{n}, {heads}, {d}] {dtype}")
-    st, sh, sd = x.stride()
-    if sd != 1 and d > 1 and n * heads:
-        raise ValueError(f"the last dimension of {name} must be contiguous")
-    return x.data_ptr(), st, sh
+def _on_stream(stream, like, fn, *args):
+    """A call on another stream than the current one: it is made current, so that the memory which the call takes
+    is that stream's and is not given away while the call still uses it."""
+    if stream.device != like.device:
+        raise ValueError(f"a stream of {stream.device} for tensors on {like.device}")
+    with _torch().cuda.stream(stream):
+        return fn(*args)
 
 
 def tq_qk_norm_rope(rope: Optional[TQRope], q, k, pos=None, wq=None, wk=None, eps: float = 1e-6,
@@ -426,32 +385,11 @@ def tq_qk_norm_rope(rope: Optional[TQRope], q, k, pos=None, wq=None, wk=None, ep
     positions (pos int64 [n]; rope None: no rotation) of q [n, Hq, d] and k
     [n, Hkv, d] (k may be None), any token and head strides.  Returns (q_out,
     k_out); the outputs may be the inputs."""
-    torch = _torch()
-    n, Hq, d = q.shape
-    dt = q.dtype
-    device = _one_device(q, k, pos, wq, wk, q_out, k_out)
-    qi = _heads("q", q, n, Hq, d, dt)
-    if q_out is None:
-        q_out = _empty_as(q, device, stream)
-        qo = q_out.data_ptr(), Hq * d, d
-    else:
-        qo = _heads("q_out", q_out, n, Hq, d, dt)
-    Hkv, ki, ko = 0, (None, 0, 0), (None, 0, 0)
-    if k is not None:
-        Hkv = k.shape[1]
-        ki = _heads("k", k, n, Hkv, d, dt)
-        if k_out is None:
-            k_out = _empty_as(k, device, stream)
-            ko = k_out.data_ptr(), Hkv * d, d
-        else:
-            ko = _heads("k_out", k_out, n, Hkv, d, dt)
-    if rope is not None and pos is None:
-        raise ValueError("a rotation needs positions")
-    _call("tq_qk_norm_rope", device, stream, None if rope is None else rope.handle, _dtype_code(q), n, d, Hq, *qi,
-          Hkv, *ki, None if pos is None else _is("pos", pos, torch.int64, (n,)),
-          None if wq is None else _is("wq", wq, dt, (d,)), None if wk is None else _is("wk", wk, dt, (d,)), eps,
-          *qo, *ko)
-    return q_out, k_out
+    fn = _bound().qk_norm_rope
+    handle = 0 if rope is None else rope.handle.value
+    if stream is not None:
+        return _on_stream(stream, q, fn, handle, q, k, pos, wq, wk, eps, q_out, k_out)
+    return fn(handle, q, k, pos, wq, wk, eps, q_out, k_out)
 
 
 class TQPaged:
@@ -464,8 +402,8 @@ class TQPaged:
         L.check("tq_paged_info", L.lib().tq_paged_info(self._h, C.byref(bw), C.byref(pw)))
         self.kp, self.vp, self.layers, self.hkv, self.page = kp, vp, layers, hkv, page
         self.block_words, self.page_words = bw.value, pw.value
-        self._rnorm = getattr(_torch(), kp.rnorm_dtype)
-        self._ws_bytes = {}  # of attention by (sequences, query heads, device), of compaction by pages
+        self._c = _bound().Paged(self._h.value, self.page_words, hkv, kp.d, kp.code_words, kp.sign_words, vp.code_words,
+                                 kp.rnorm_dtype == "float16")
 
     @property
     def handle(self):
@@ -480,6 +418,7 @@ class TQPaged:
         if self._h:
             L.lib().tq_paged_destroy(self._h)
             self._h = C.c_void_p()
+            self._c.handle = 0
 
     def __del__(self):
         try:
@@ -488,53 +427,18 @@ class TQPaged:
             pass
 
 
-def _pool(pg, pool):
-    if pool.dtype != _torch().int32 or pool.dim() != 2 or pool.shape[1] != pg.page_words or not pool.is_contiguous():
-        raise ValueError(f"pool must be contiguous int32 [n_pages, {pg.page_words}]")
-    return pool.data_ptr(), pool.shape[0]
-
-
-def _table(name, t, B):
-    """Pointer, row stride and width of a page table (rows contiguous, any stride between them)."""
-    if t.dtype != _torch().int32 or t.dim() != 2 or t.shape[0] != B:
-        raise ValueError(f"{name} must be int32 [{B}, max_pages]")
-    width = t.shape[1]
-    ld, one = t.stride()
-    if B and (one != 1 and width > 1 or B > 1 and ld < width):
-        raise ValueError(f"the rows of {name} must be contiguous and apart")
-    return t.data_ptr(), max(ld, width), width
-
-
-def _encoded(name, t, dtype, n):
-    if t.dtype != dtype or t.numel() != n or not t.is_contiguous():
-        raise ValueError(f"{name} must be {n} contiguous {dtype}")
-    return t.data_ptr()
-
-
 def tq_paged_append(pg: TQPaged, pool, layer: int, keys, values, start, tables, cu=None, stream=None):
-    """Write encoded tokens into the pages of a layer.  keys = (codes, signs,
-    norms, rnorms) of tq_encode_prod and values = (codes, norms) of
-    tq_encode_mse (ROW layout) for rows [n_tok, Hkv]; the tokens cu[b] ..
+    """Write encoded tokens into the pages of one layer: keys = (codes, signs,
+    norms, residual norms) of tq_encode_prod and values = (codes, norms) of
+    tq_encode_mse (ROW) for vectors [n_tok, hkv, d]; sequence b's tokens cu[b] ..
     cu[b + 1] - 1 (cu int32 [B + 1]; None: token b) go to the positions from
     start[b] (int32 [B]) on of sequence b, whose pages are tables[b]."""
-    torch = _torch()
-    i32, f32 = torch.int32, torch.float32
+    fn = _bound().paged_append
     kcodes, ksigns, knorms, krnorms = keys
     vcodes, vnorms = values
-    B, rows = start.shape[0], knorms.numel()
-    n_tok = rows // pg.hkv
-    if rows != n_tok * pg.hkv:
-        raise ValueError(f"{rows} rows are no multiple of {pg.hkv} heads")
-    if cu is None and n_tok != B:
-        raise ValueError(f"{n_tok} tokens for {B} sequences need cu")
-    device = _one_device(pool, kcodes, ksigns, knorms, krnorms, vcodes, vnorms, start, tables, cu)
-    _call("tq_paged_append", device, stream, pg.handle, *_pool(pg, pool), layer,
-          _encoded("key codes", kcodes, i32, rows * pg.kp.code_words),
-          _encoded("key signs", ksigns, i32, rows * pg.kp.sign_words), _encoded("key norms", knorms, f32, rows),
-          _encoded("residual norms", krnorms, pg._rnorm, rows),
-          _encoded("value codes", vcodes, i32, rows * pg.vp.code_words), _encoded("value norms", vnorms, f32, rows),
-          n_tok, B, None if cu is None else _is("cu", cu, i32, (B + 1,)), _is("start", start, i32, (B,)),
-          *_table("tables", tables, B))
+    if stream is not None:
+        return _on_stream(stream, pool, fn, pg._c, pool, layer, kcodes, ksigns, knorms, krnorms, vcodes, vnorms, start, tables, cu)
+    return fn(pg._c, pool, layer, kcodes, ksigns, knorms, krnorms, vcodes, vnorms, start, tables, cu)
 
 
 def tq_paged_attention_workspace_size(pg: TQPaged, B: int, Hq: int) -> int:
@@ -544,48 +448,28 @@ def tq_paged_attention_workspace_size(pg: TQPaged, B: int, Hq: int) -> int:
     return need.value
 
 
-def tq_paged_attention(pg: TQPaged, q, pool, layer: int, lens, tables, scale: float, out=None, lse=None,
-                       want_lse: bool = False, ws=None, stream=None):
-    """One query token per sequence: q [B, Hq, d] (fp32, fp16 or bf16; any
-    stride between sequences) over the first lens[b] (int32 [B]) tokens of the
-    pages tables[b].  Returns out [B, Hq, d] of q's dtype, or (out, lse [B, Hq]
-    fp32) with want_lse."""
-    torch = _torch()
-    B, Hq, d = q.shape
-    if d != pg.kp.d:
-        raise ValueError(f"last dimension {d} != d {pg.kp.d}")
-    sb, sh, sd = q.stride()
-    if (sd != 1 or sh != d or (B > 1 and sb < Hq * d)) and q.numel():
-        q = q.contiguous()
-        sb = Hq * d
-    device = _one_device(q, pool, lens, tables, out, lse, ws)
-    if out is None:
-        out = _empty_as(q, device, stream)
-    if lse is None and want_lse:
-        lse = _empty((B, Hq), torch.float32, device, stream)
-    if ws is None:
-        need = pg._ws_bytes.get((B, Hq, device.index))
-        if need is None:
-            with torch.cuda.device(device):
-                need = pg._ws_bytes[B, Hq, device.index] = tq_paged_attention_workspace_size(pg, B, Hq)
-        ws = _empty(need, torch.uint8, device, stream)
-    _call("tq_paged_attention", device, stream, pg.handle, q.data_ptr(), _dtype_code(q), max(sb, Hq * d), B, Hq,
-          *_pool(pg, pool), layer, _is("lens", lens, torch.int32, (B,)), *_table("tables", tables, B), scale,
-          _is("out", out, q.dtype, (B, Hq, d)), None if lse is None else _is("lse", lse, torch.float32, (B, Hq)),
-          None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel() * ws.element_size())
-    return (out, lse) if want_lse else out
+def tq_paged_attention(pg: TQPaged, q, pool, layer: int, lens, tables, scale: float, out=None, lse=None, ws=None,
+                       stream=None, want_lse: bool = False):
+    """Attention of one query token per sequence, q [B, Hq, d] (fp32, fp16 or
+    bf16; any stride between sequences), over the first lens[b] (int32 [B])
+    tokens of the pages tables[b] of one layer.  Returns out [B, Hq, d], or
+    (out, lse [B, Hq]) with want_lse."""
+    fn = _bound().paged_attention
+    if stream is not None:
+        got = _on_stream(stream, q, fn, pg._c, q, pool, layer, lens, tables, scale, out, lse, ws, want_lse)
+    else:
+        got = fn(pg._c, q, pool, layer, lens, tables, scale, out, lse, ws, want_lse)
+    return got if want_lse else got[0]
 
 
 def tq_paged_fork(pg: TQPaged, pool, tables, lens, parents, children, fresh, stream=None):
     """Make sequences children[i] copies of parents[i]: table rows, lengths and
     (into page fresh[i]) the partly filled last page.  All int32; tables and
     lens are updated in place."""
-    i32 = _torch().int32
-    B, n = lens.shape[0], parents.shape[0]
-    device = _one_device(pool, tables, lens, parents, children, fresh)
-    _call("tq_paged_fork", device, stream, pg.handle, *_pool(pg, pool), *_table("tables", tables, B),
-          _is("lens", lens, i32, (B,)), B, _is("parents", parents, i32, (n,)), _is("children", children, i32, (n,)),
-          _is("fresh", fresh, i32, (n,)), n)
+    fn = _bound().paged_fork
+    if stream is not None:
+        return _on_stream(stream, pool, fn, pg._c, pool, tables, lens, parents, children, fresh)
+    return fn(pg._c, pool, tables, lens, parents, children, fresh)
 
 
 def tq_paged_compact_workspace_size(n_pages: int) -> int:
@@ -598,26 +482,10 @@ def tq_paged_compact(pg: TQPaged, pool, tables, lens, tables_out=None, n_used=No
     """Move the pages that the sequences use to the lowest numbers and rewrite
     the tables (into tables_out; None: in place).  Returns n_used (int32 [1], on
     the device): pages n_used and behind are free."""
-    torch = _torch()
-    B = lens.shape[0]
-    device = _one_device(pool, tables, lens, tables_out, n_used, ws)
-    if tables_out is None:
-        tables_out = tables
-    elif tables_out.shape != tables.shape or tables_out.stride() != tables.stride():
-        raise ValueError("tables_out must have the shape and strides of tables")
-    if n_used is None:
-        n_used = _empty(1, torch.int32, device, stream)
-    if ws is None:
-        need = pg._ws_bytes.get(pool.shape[0])
-        if need is None:
-            need = pg._ws_bytes[pool.shape[0]] = tq_paged_compact_workspace_size(pool.shape[0])
-        ws = _empty(need, torch.uint8, device, stream)
-    tab, ld, width = _table("tables", tables, B)
-    out = tab if tables_out is tables else _table("tables_out", tables_out, B)[0]
-    _call("tq_paged_compact", device, stream, pg.handle, *_pool(pg, pool), tab, out, ld, width,
-          _is("lens", lens, torch.int32, (B,)), B, _is("n_used", n_used, torch.int32, (1,)), ws.data_ptr(),
-          ws.numel() * ws.element_size())
-    return n_used
+    fn = _bound().paged_compact
+    if stream is not None:
+        return _on_stream(stream, pool, fn, pg._c, pool, tables, lens, tables_out, n_used, ws)
+    return fn(pg._c, pool, tables, lens, tables_out, n_used, ws)
 
 
 def tq_check_wait_expiry(budget_cycles: int, stream=None):

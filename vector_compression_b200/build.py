@@ -3,7 +3,9 @@
     python -m vector_compression_b200.build [--force]
 
 The shared library is written next to this file so that it travels with the
-source tree; it is rebuilt when any source under csrc/ or include/ is newer.
+source tree, and with it _torch_binding.so, the calls on torch tensors that run
+once per layer and step; both are rebuilt when any source under csrc/ or
+include/ is newer.
 """
 from __future__ import annotations
 
@@ -17,6 +19,9 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libtq.so")
+# the calls on torch tensors, a Python module that is linked against libtq.so
+BINDING_SRC = os.path.join(CSRC, "binding", "tq_torch.cpp")
+BINDING = os.path.join(HERE, "_torch_binding.so")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -36,10 +41,28 @@ def deps():
 
 
 def needs_build() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return True
-    t = os.path.getmtime(LIB)
-    return any(os.path.getmtime(f) > t for f in deps())
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
+    return any(os.path.getmtime(f) > t for f in deps() + [BINDING_SRC])
+
+
+def binding_commands(obj: str, out: str):
+    """Compile and link commands of the binding (torch's headers and libraries, this interpreter's)."""
+    import sysconfig
+
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc())) if os.path.sep in nvcc() else "/usr/local/cuda"
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    compile_ = ["g++", "-O2", "-std=c++17", "-fPIC", "-DTORCH_EXTENSION_NAME=_torch_binding",
+                f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+                *[x for i in inc for x in ("-isystem", i)], "-c", BINDING_SRC, "-o", obj]
+    link = ["g++", "-shared", "-o", out, obj, "-L" + HERE, "-l:libtq.so", "-Wl,-rpath,$ORIGIN",
+            "-L" + os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu", "-ltorch_python"]
+    return compile_, link
 
 
 def nvcc() -> str:
@@ -57,6 +80,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
     t0 = time.time()
     procs = []
     objs = []
+    binding_obj = os.path.join(objdir, "tq_torch.cpp.o")
+    compile_binding, link_binding = binding_commands(binding_obj, BINDING + ".tmp")
+    procs.append((compile_binding, subprocess.Popen(compile_binding, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     for src in sources():
         obj = os.path.join(objdir, os.path.basename(src) + ".o")
         objs.append(obj)
@@ -76,6 +102,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
             "-lcudart"]
     subprocess.run(link, check=True)
     os.replace(tmp, LIB)
+    subprocess.run(link_binding, check=True)
+    os.replace(BINDING + ".tmp", BINDING)
     if verbose:
         print(f"built {LIB} in {time.time() - t0:.1f}s")
     return LIB
