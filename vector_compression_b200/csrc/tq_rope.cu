@@ -242,7 +242,12 @@ __global__ void __launch_bounds__(256, V == 8 ? 2 : 3) norm_rope_kernel(const __
   int a = 0, b = -1;
   if (there) chunk_at<V, PAIRS>(lane, np, A, a, b);
   const bool both = b >= 0;
+  // a group with heads of both sides: fp32's sines are made once; the 16-bit ones are short, and eight pairs of them
+  // held over both sides spill
+  constexpr bool kOnce = sizeof(T) == 4;
   const uint64_t pos = turn ? (uint64_t)A.pos[tok] : 0;
+  float co1[V] = {}, si1[V] = {};
+  if (kOnce && turn) turns<T, V>(A, lane, pos, co1, si1);
   // rows in flight against registers: four of eight-element vectors at two blocks per SM (16384 x 40 x 128 fp16: 63 us,
   // with norms 70) or two of the smaller ones at three; two at three blocks are 63 and 75 there, four spill
   constexpr int U = V == 8 ? 4 : 2;
@@ -255,7 +260,12 @@ __global__ void __launch_bounds__(256, V == 8 ? 2 : 3) norm_rope_kernel(const __
     T* y = static_cast<T*>(s.y) + tok * s.yt + first * s.yh + a;
     Factors<V> f;
     float co[V] = {}, si[V] = {};
-    if (turn) turns<T, V>(A, lane, pos, co, si);
+    if constexpr (kOnce) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) co[i] = co1[i], si[i] = si1[i];
+    } else if (turn) {
+      turns<T, V>(A, lane, pos, co, si);
+    }
     if (s.w) {
       float g0[V] = {}, g1[V] = {};
       if (there) load<T, V>(static_cast<const T*>(s.w) + a, g0);
