@@ -360,7 +360,7 @@ _binding = None
 
 
 def _bound():
-    """The calls on tensors (csrc/binding/tq_torch.cpp); loads libtq.so with it."""
+    """The calls on tensors (binding/tq_torch.cpp); loads libtq.so with it."""
     global _binding
     if _binding is None:
         L.lib()

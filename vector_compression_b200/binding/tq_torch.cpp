@@ -12,7 +12,7 @@
 #include <string>
 #include <tuple>
 
-#include "../../../include/tq.h"
+#include "../../include/tq.h"
 
 namespace py = pybind11;
 

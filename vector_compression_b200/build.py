@@ -4,7 +4,7 @@
 
 The shared library is written next to this file so that it travels with the
 source tree, and with it _torch_binding.so, the calls on torch tensors that run
-once per layer and step; both are rebuilt when any source under csrc/ or
+once per layer and step; both are rebuilt when any source under csrc/, binding/ or
 include/ is newer.
 """
 from __future__ import annotations
@@ -20,7 +20,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libtq.so")
 # the calls on torch tensors, a Python module that is linked against libtq.so
-BINDING_SRC = os.path.join(CSRC, "binding", "tq_torch.cpp")
+BINDING_SRC = os.path.join(HERE, "binding", "tq_torch.cpp")
 BINDING = os.path.join(HERE, "_torch_binding.so")
 
 NVCC_FLAGS = [
