@@ -453,11 +453,11 @@ struct Plan {
 
 size_t round256(size_t b) { return (b + 255) & ~(size_t)255; }
 
-Plan plan_of(const tq_paged* pg, int B, int Hq) {
+Plan plan_of(const tq_paged* pg, int B, int Hq, bool fine) {
   const Layout& L = pg->lay;
   const int G = Hq / L.hkv;
   Plan p = {};
-  p.tc = tc_shape(pg->kq.k, L.kv, pg->kq.m, L.dp, G);
+  p.tc = tc_shape(pg->kq.k, L.kv, pg->kq.m, L.dp, G, fine);
   const size_t heads = (size_t)B * Hq;
   if (p.tc.ctas_per_sm) {
     const int hn = 4 * p.tc.nt, groups = (G + hn - 1) / hn;
@@ -514,7 +514,8 @@ extern "C" tq_status tq_paged_attention_workspace_size(const tq_paged* pg, int B
   using namespace tq::paged;
   if (!pg || !bytes || B < 0 || B > (1 << 20) || Hq < pg->lay.hkv || Hq % pg->lay.hkv) return TQ_ERR_INVALID_ARG;
   if (Hq / pg->lay.hkv > kMaxGroup || too_wide(pg, Hq / pg->lay.hkv)) return TQ_ERR_UNSUPPORTED;
-  *bytes = B == 0 ? 0 : plan_of(pg, B, Hq).all();
+  // for queries of every type
+  *bytes = B == 0 ? 0 : std::max(plan_of(pg, B, Hq, false).all(), plan_of(pg, B, Hq, true).all());
   return TQ_OK;
 }
 
@@ -538,7 +539,7 @@ extern "C" tq_status tq_paged_attention(const tq_paged* pg, const void* q, tq_dt
     return TQ_ERR_INVALID_ARG;
   if ((int64_t)B * Hq > 0x7fffffffll) return TQ_ERR_UNSUPPORTED;
   if (!ws || ws_bytes < need || !al256(ws)) return TQ_ERR_WORKSPACE;
-  const Plan z = plan_of(pg, B, Hq);
+  const Plan z = plan_of(pg, B, Hq, fine_sums(dt));
   char* w = static_cast<char*>(ws);
   AttnArgs a = {};
   a.L = L;

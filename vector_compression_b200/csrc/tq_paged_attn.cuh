@@ -159,6 +159,9 @@ __device__ __forceinline__ void store_out(const AttnArgs& A, int64_t i, float v)
   else static_cast<__nv_bfloat16*>(A.out)[i] = __float2bfloat16_rn(v);
 }
 
+// Whether the values' sums have to be as exact as fp32's: an output of 16 bits hides what is lost in them.
+inline bool fine_sums(int dt) { return dt == TQ_F32; }
+
 // The tensor-core kernel (tq_paged_attn_tc.cuh): what it needs to know of a
 // shape, and its launch.  ctas == 0: not a shape of it.
 struct TcShape {
@@ -168,13 +171,13 @@ struct TcShape {
   int steps;       // MMA steps over q' and over u
   int smem;        // bytes of a CTA
 };
-TcShape tc_shape(int kk, int kv, int m, int dp, int G);
+TcShape tc_shape(int kk, int kv, int m, int dp, int G, bool fine);
 cudaError_t tc_launch(const AttnArgs& a, const QParams& kq, const QParams& vq, const TcShape& s, int ctas, cudaStream_t st);
 
 // Codebooks as the tensor-core kernel takes them.
 struct TcBooks {
   float kalpha[4];      // odd-subset coefficients of the key codebook
-  uint32_t hi[2], lo[2];  // bytes of the 16-bit value levels
+  uint32_t hi[2], lo[2], th[2];  // bytes of the value levels, of 16 bits or (th too) of 24
   float unit;           // value of one step of them
 };
 

@@ -29,6 +29,15 @@
 // those of q', u (2^-24 to 2^-21 of the largest entry by the bit's place), the
 // levels and the weights (2^-16 of the largest), and fp32 outside.
 //
+// 16-bit levels and weights put an output 2e-5 to 6e-5 off (of its 2-norm), a
+// tenth of the rounding to fp16 that follows, and a hundred times what fp32
+// holds.  So fp32 outputs take the FINE form: levels of 24 bits and weights of
+// 23 (what a float's significand gives without further instructions), three
+// bytes each, of whose nine products the one below 2^-30 is left out: 2e-7 to
+// 5e-7, as fp32 sums.  The third byte of the weights is a tile of its own, laid
+// out as that of the queries.  The case below takes 95 us so, 48 sequences of 0
+// to 6000 tokens with 2 x 8 heads 41 us instead of 38.
+//
 // What bounds it (8 sequences of 31 thousand tokens, 8 KV heads of 4 query
 // heads, d = m = 128, 3 bits: 78 us, 2.7 TB/s, of 33 us that the bytes take): the
 // ALU (51% busy: masks, permutes) and the tensor pipe (39%), which overlap only
@@ -42,7 +51,7 @@ namespace tq {
 namespace paged {
 namespace tc {
 
-template <int KK, int KV, int NT, int DP, int MQ>
+template <int KK, int KV, int NT, int DP, int MQ, bool FINE>
 struct Shape {
   static constexpr int WPP = DP / 32, SW = MQ / 32, NK = KK * WPP + SW;
   static constexpr int GR = NK % 4 == 0 ? 4 : 2;
@@ -53,8 +62,8 @@ struct Shape {
   static constexpr int VB = KV * DP + 32 + 8;    // and values: 8 mod 32, so that four blocks are on different banks
   static constexpr int WC = 36;                  // words of a column of weights (32 and a gap)
   // the group's scores (a thread's own four of each block), and then its weights
-  static constexpr int XW = 4 * 32 * 4 * NT;
-  static_assert(XW >= 8 * NT * WC, "the weights fit the scores' place");
+  static constexpr int WT = NT + FINE;           // tiles of the weights
+  static constexpr int XW = 4 * 32 * 4 * NT > 8 * WT * WC ? 4 * 32 * 4 * NT : 8 * WT * WC;
   // the running sums: in shared memory the loop over coordinates need not be unrolled (a fourth of the code, which a
   // short call fetches for one use) and 16 registers a tile are free; at d_pad 256 two warps of an SM's eight would not fit
   static constexpr bool O_SMEM = DP < 256;
@@ -124,24 +133,20 @@ __device__ __forceinline__ uint32_t selectors(const uint32_t (&w)[KV], int s) {
   return (a & 0x33333333u) | (b & 0x44444444u);
 }
 
-// hi and lo bytes of four tokens' levels; x: their selectors in the low 16 bits
-// (KV = 4: without the signs), neg: theirs as selectors of a byte 0xff.
+// A byte of four tokens' levels; x: their selectors in the low 16 bits (KV = 4:
+// without the signs), flip: 0xff where the level is below zero.
 template <int KV>
-__device__ __forceinline__ void levels(const TcBooks& K, uint32_t x, uint32_t neg, uint32_t& hi, uint32_t& lo) {
-  hi = __byte_perm(K.hi[0], KV >= 3 ? K.hi[1] : 0u, x);
-  lo = __byte_perm(K.lo[0], KV >= 3 ? K.lo[1] : 0u, x);
-  if constexpr (KV == 4) {
-    const uint32_t s = __byte_perm(0x0000ff00u, 0u, neg);
-    hi ^= s;
-    lo ^= s;
-  }
+__device__ __forceinline__ uint32_t levels(const uint32_t (&book)[2], uint32_t x, uint32_t flip) {
+  const uint32_t v = __byte_perm(book[0], KV >= 3 ? book[1] : 0u, x);
+  return KV == 4 ? v ^ flip : v;
 }
 
-template <int KK, int KV, int NT, int DP, int MQ>
-__global__ void __launch_bounds__(64, Shape<KK, KV, NT, DP, MQ>::CTAS)
+template <int KK, int KV, int NT, int DP, int MQ, bool FINE>
+__global__ void __launch_bounds__(64, Shape<KK, KV, NT, DP, MQ, FINE>::CTAS)
     attention_tc_kernel(const __grid_constant__ AttnArgs A, const __grid_constant__ TcBooks K) {
-  using S = Shape<KK, KV, NT, DP, MQ>;
-  constexpr int WPP = S::WPP, SW = S::SW, NQ = S::NQ, FK = S::FK, STEPS = S::STEPS;
+  using S = Shape<KK, KV, NT, DP, MQ, FINE>;
+  constexpr int WPP = S::WPP, SW = S::SW, NQ = S::NQ, FK = S::FK, STEPS = S::STEPS, WT = S::WT;
+  constexpr float kWeight = FINE ? 8388607.f : 65535.f;  // the largest weight of a group
   extern __shared__ __align__(128) unsigned char smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, tig = lane & 3;
@@ -229,7 +234,8 @@ __global__ void __launch_bounds__(64, Shape<KK, KV, NT, DP, MQ>::CTAS)
   // thread (g, tig): the tokens 16 h + 4 (r ^ h) + s, r = 0..3, of a block (rows g and g + 8 of two m-tiles;
   // eight neighbouring tokens modulo 8 per row set, so that their words are on different banks)
   const int th = g >> 2, ts = g & 3;
-  const uint32_t pack_sel = th ? 0x1504u : 0x5140u;  // bytes lo, lo, hi, hi of two tokens, in the order of i
+  const uint32_t pack_sel = th ? 0x1504u : 0x5140u;  // bytes 0, 0, 1, 1 of two tokens, in the order of i
+  const uint32_t pack_top = th ? 0x0026u : 0x0062u;  // byte 2 of them
   const int wt = WPP == 2 ? tig & 1 : tig, ws = MQ == 64 ? tig & 1 : tig;  // this thread's word of a plane, of the signs
   const int ksh = WPP == 2 ? 4 * (tig >> 1) : 0, ssh = MQ == 64 ? 4 * (tig >> 1) : 0;
 
@@ -423,26 +429,33 @@ __global__ void __launch_bounds__(64, Shape<KK, KV, NT, DP, MQ>::CTAS)
       if (KV == 4) w_run[n] += wsum;
 #pragma unroll
       for (int k = 4; k < 32; k *= 2) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, k));
-      const float inv = big > 1e-33f ? 65535.f / big : 0.f;
-      back[n] = big > 1e-33f ? big * (256.f / 65535.f) * K.unit : 0.f;
+      const float inv = big > 1e-33f ? kWeight / big : 0.f;
+      back[n] = big > 1e-33f ? big * ((FINE ? 0x1p24f : 0x1p8f) / kWeight) * K.unit : 0.f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        // the integer part in the low 16 bits
+        // the integer part in the low 16 or 23 bits (2^23 itself: 2^7 in byte 2)
         uint32_t b[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) b[r] = __float_as_uint(fmaf(x[n][i][r], inv, 8388608.f));
         const uint32_t lh0 = __byte_perm(b[0], b[1], pack_sel), lh1 = __byte_perm(b[2], b[3], pack_sel);
         uint32_t* col = wb + (8 * n + 2 * tig) * S::WC + 8 * i + 2 * ts + th;
-        col[0] = __byte_perm(lh0, lh1, 0x7632);
-        col[S::WC] = __byte_perm(lh0, lh1, 0x5410);
+        const uint32_t b1 = __byte_perm(lh0, lh1, 0x7632), b0 = __byte_perm(lh0, lh1, 0x5410);
+        if constexpr (FINE) {
+          col[0] = __byte_perm(__byte_perm(b[0], b[1], pack_top), __byte_perm(b[2], b[3], pack_top), 0x5410);
+          col[S::WC] = b1;
+          col[(8 * (NT - n) + n) * S::WC] = b0;  // column 2 tig + n of the last tile
+        } else {
+          col[0] = b1;
+          col[S::WC] = b0;
+        }
       }
     }
     __syncwarp();
 
     // ---------------- values
-    uint2 bw[NT][4];
+    uint2 bw[WT][4];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
+    for (int n = 0; n < WT; ++n) {
       const uint4* col = reinterpret_cast<const uint4*>(wb + (8 * n + g) * S::WC + 8 * tig);
       const uint4 a = col[0], b = col[1];
       bw[n][0] = make_uint2(a.x, a.y);
@@ -462,37 +475,52 @@ __global__ void __launch_bounds__(64, Shape<KK, KV, NT, DP, MQ>::CTAS)
         w[2][q] = v.z;
         w[3][q] = v.w;
       }
-      int ah[2][NT][4], al[2][NT][4];  // rows g and g + 8 of m-tile mt: coordinates 2 mt and 2 mt + 1 of the four
+      // rows g and g + 8 of m-tile mt: coordinates 2 mt and 2 mt + 1 of the four; the levels' bytes
+      int ah[2][WT][4], al[2][WT][4], at[2][NT][4];
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < WT; ++n)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) ah[mt][n][k] = al[mt][n][k] = 0;
+          for (int k = 0; k < 4; ++k) {
+            ah[mt][n][k] = al[mt][n][k] = 0;
+            if (n < NT) at[mt][n][k] = 0;
+          }
 #pragma unroll
       for (int s = 0; s < 4; ++s)
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
-          uint32_t h[2][2], l[2][2];
+          uint32_t h[2][2], l[2][2], t[2][2];
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
             const uint32_t y = selectors<KV>(w[2 * mt + r], s);
             const uint32_t neg = KV == 4 ? (y >> 3) & 0x11111111u : 0u;
             const uint32_t z = KV == 4 ? y & 0x77777777u : y;
-            levels<KV>(K, z, neg, h[r][0], l[r][0]);
-            levels<KV>(K, z >> 16, neg >> 16, h[r][1], l[r][1]);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              const uint32_t flip = KV == 4 ? __byte_perm(0x0000ff00u, 0u, neg >> (16 * half)) : 0u;
+              h[r][half] = levels<KV>(K.hi, z >> (16 * half), flip);
+              l[r][half] = levels<KV>(K.lo, z >> (16 * half), flip);
+              if (FINE) t[r][half] = levels<KV>(K.th, z >> (16 * half), flip);
+            }
           }
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
+          for (int n = 0; n < WT; ++n) {
             mma_su(ah[mt][n], h[0][0], h[1][0], h[0][1], h[1][1], bw[n][s]);
             mma_uu(al[mt][n], l[0][0], l[1][0], l[0][1], l[1][1], bw[n][s]);
+            if (FINE && n < NT) mma_uu(at[mt][n], t[0][0], t[1][0], t[0][1], t[1][1], bw[n][s]);
           }
         }
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        // in units of 2^8: what the shift drops is below 2^-8 of a unit, of 2^30 where the weights are large
         auto sum = [&](int mt, int r) {
-          return (float)(256 * ah[mt][n][2 * r] + ah[mt][n][2 * r + 1] + al[mt][n][2 * r] + (al[mt][n][2 * r + 1] >> 8));
+          const int hh = ah[mt][n][2 * r], hl = ah[mt][n][2 * r + 1], lh = al[mt][n][2 * r], ll = al[mt][n][2 * r + 1];
+          // in units of 2^8: what the shift drops is below a unit, of 2^30 where the weights are large
+          if (!FINE) return (float)(256 * hh + hl + lh + (ll >> 8));
+          // in units of 2^24, of 2^29 where the weights are large; the two bytes below are of 2^16 and 2^8, and what the
+          // shift drops is below 2^16
+          const int below = ah[mt][NT][2 * r + n] + ll + at[mt][n][2 * r] + ((al[mt][NT][2 * r + n] + at[mt][n][2 * r + 1]) >> 8);
+          return fmaf((float)below, 0x1p-8f, (float)(256 * hh + hl + lh));
         };
         float4 t = o_get(c, n);
         t.x = fmaf(back[n], sum(0, 0), t.x);
@@ -553,14 +581,20 @@ __global__ void __launch_bounds__(64, Shape<KK, KV, NT, DP, MQ>::CTAS)
 }
 
 // One (d_pad, m, key bits) per source file.
-template <int KK, int KV, int NT, int DP, int MQ>
-cudaError_t launch_one(const AttnArgs& a, const TcBooks& k, int ctas, cudaStream_t st) {
-  using S = Shape<KK, KV, NT, DP, MQ>;
-  auto kern = attention_tc_kernel<KK, KV, NT, DP, MQ>;
+template <int KK, int KV, int NT, int DP, int MQ, bool FINE>
+cudaError_t launch_form(const AttnArgs& a, const TcBooks& k, int ctas, cudaStream_t st) {
+  using S = Shape<KK, KV, NT, DP, MQ, FINE>;
+  auto kern = attention_tc_kernel<KK, KV, NT, DP, MQ, FINE>;
   // function attributes are per device: set on every call (a cheap host call)
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
   if (e != cudaSuccess) return e;
   return launch_after(kern, dim3(ctas), 32 * S::WARPS, S::SMEM, st, a, k);
+}
+
+template <int KK, int KV, int NT, int DP, int MQ>
+cudaError_t launch_one(const AttnArgs& a, const TcBooks& k, int ctas, cudaStream_t st) {
+  return fine_sums(a.dt) ? launch_form<KK, KV, NT, DP, MQ, true>(a, k, ctas, st)
+                         : launch_form<KK, KV, NT, DP, MQ, false>(a, k, ctas, st);
 }
 
 template <int KK, int DP, int MQ>
