@@ -275,13 +275,21 @@ def _prepare_rope(c, g):
     f, st["mscale"] = _frequencies(c)
     st["f"] = torch.tensor(f, device=SM)
     if own:
+        st["rope"] = _rope(c)
+    return st
+
+
+def _rope(c, _handles={}):
+    """The rotation's handle, kept as _paged's are."""
+    key = tuple(c[k] for k in ("rot", "base", "layout", "scaling"))
+    if key not in _handles:
         import vector_compression_b200 as tq
 
         kind, more = dict(none=(tq.ROPE_PLAIN, {}), linear=(tq.ROPE_LINEAR, dict(factor=4.0)),
                           bands=(tq.ROPE_BANDS, dict(factor=8.0, orig_len=8192, low=1.0, high=4.0)),
                           yarn=(tq.ROPE_YARN, dict(factor=16.0, orig_len=4096, low=1.0, high=32.0)))[c["scaling"]]
-        st["rope"] = tq.TQRope(c["rot"], c["base"], interleaved=c["layout"] == "pairs", scaling=kind, **more)
-    return st
+        _handles[key] = tq.TQRope(c["rot"], c["base"], interleaved=c["layout"] == "pairs", scaling=kind, **more)
+    return _handles[key]
 
 
 def _rope_plain(x, w, s):
@@ -329,14 +337,19 @@ def _exact_rope(s):
 
 # ----------------------------------------------------------------------------------------------- append
 
-def _paged(c):
-    import vector_compression_b200 as tq
+def _paged(c, _handles={}):
+    """The cache's handle.  It says nothing of the inputs: a program makes its quantizers (whose codebooks take
+    milliseconds) when it starts, and so this keeps one of each kind, as _tables does for the plain form."""
+    key = tuple(c[k] for k in ("d", "m", "bits", "r16", "layers", "hkv", "page"))
+    if key not in _handles:
+        import vector_compression_b200 as tq
 
-    z = _quantizer(c)
-    mode = tq.MODE_PROD | (tq.STORE_RNORM_F16 if c["r16"] else 0)
-    kp = tq.TQParams(c["d"], c["bits"], mode, tq.ROT_HADAMARD, m=c["m"], signs=z["dk"], S=z["s"])
-    vp = tq.TQParams(c["d"], c["bits"], tq.MODE_MSE, tq.ROT_HADAMARD, signs=z["dv"])
-    return tq.TQPaged(kp, vp, layers=c["layers"], hkv=c["hkv"], page=c["page"])
+        z = _quantizer(c)
+        mode = tq.MODE_PROD | (tq.STORE_RNORM_F16 if c["r16"] else 0)
+        kp = tq.TQParams(c["d"], c["bits"], mode, tq.ROT_HADAMARD, m=c["m"], signs=z["dk"], S=z["s"])
+        vp = tq.TQParams(c["d"], c["bits"], tq.MODE_MSE, tq.ROT_HADAMARD, signs=z["dv"])
+        _handles[key] = tq.TQPaged(kp, vp, layers=c["layers"], hkv=c["hkv"], page=c["page"])
+    return _handles[key]
 
 
 def _prepare_append(c, g):
