@@ -430,7 +430,8 @@ tq_status tq_qk_norm_rope(const tq_rope* rope, tq_dtype dt, int64_t n_tok, int d
  *                            32 of word 2
  *                  k = 4     bits 4 i .. 4 i + 3 of word s: 0..7 for index 8 +
  *                            x, 8 + x for index 7 - x
- *   value norms  float [32], not negative
+ *   value norms  float [32], not negative; a token's that is not finite makes
+ *                the outputs of its KV head's query heads NaN
  *
  * A page table is DEVICE int32 [B][table_ld >= max_pages]: entry i of row b is
  * the page of tokens [i page, (i + 1) page) of sequence b.  A page may stand

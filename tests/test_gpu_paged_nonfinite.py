@@ -1,0 +1,56 @@
+"""Norms of tokens that are not finite: what they do to their own KV head's outputs does not depend on which kernel a
+shape takes, and nothing else notices."""
+import numpy as np
+import pytest
+import torch
+
+import vector_compression_b200 as tq
+from tests.paged_ref import Model
+from tests.test_gpu_paged import DEV, i32, ints, quantizers, random_cache
+
+pytestmark = pytest.mark.gpu
+
+SHAPES = [
+    # d, bits, vbits, m, r16, G: the tensor-core kernel's shapes (each value width, one and two tiles of heads) ...
+    (128, 3, 3, 128, False, 4), (128, 3, 1, 64, True, 7), (64, 2, 4, 64, False, 8), (64, 4, 2, 64, False, 2),
+    (192, 3, 4, 256, False, 6),
+    # ... and others
+    (128, 5, 3, 128, False, 4), (64, 3, 4, 32, True, 3),
+]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_norms_that_are_not_finite(shape, dtype):
+    d, bits, vbits, m, r16, G = shape
+    kp, vp, _, _ = quantizers(d, bits, m, vbits, r16)
+    hkv, page = 2, 64
+    pg, model = tq.TQPaged(kp, vp, 1, hkv, page), Model(kp, vp, 1, hkv, page)
+    rng = np.random.default_rng(d + G)
+    lens = [330, 77, 1, 200]
+    pool, tables = random_cache(rng, model, lens, 6, 0)
+    q = torch.from_numpy(rng.standard_normal((4, hkv * G, d))).to(DEV).to(dtype)
+
+    def call(pool):
+        return tq.tq_paged_attention(pg, q, i32(pool), 0, ints(lens), ints(tables), d ** -0.5, want_lse=True)
+
+    clean, clean_lse = call(pool)
+    assert bool(torch.isfinite(clean).all()) and bool(torch.isfinite(clean_lse).all())
+    # first and last token, inside a group and at its end, beside a slot without a token
+    for b, t, h in ((0, 0, 1), (0, 329, 0), (0, 127, 0), (1, 76, 1), (2, 0, 0), (3, 150, 1)):
+        mine = torch.zeros(4, hkv * G, dtype=torch.bool, device=DEV)
+        mine[b, h * G:(h + 1) * G] = True
+        for part in ("vn", "kn", "kr"):
+            for bad in (np.nan, np.inf) if part == "vn" else (np.nan,):
+                p = pool.copy()
+                rec = model.record(p, tables[b, t // page], 0, h, t % page // 32)
+                if part == "kr" and r16:
+                    rec[model.kr:model.v].view(np.float16)[t % 32] = bad
+                else:
+                    rec.view(np.float32)[dict(vn=model.vn, kn=model.kn, kr=model.kr)[part] + t % 32] = bad
+                got, lse = call(p)
+                assert bool(torch.isnan(got[mine]).all()), (b, t, h, part, bad)
+                assert torch.equal(got[~mine], clean[~mine]) and torch.equal(lse[~mine], clean_lse[~mine])
+                # the softmax does not know of the values
+                assert torch.equal(lse, clean_lse) if part == "vn" else bool(torch.isnan(lse[mine]).all())
+    tq.tq_sync_check()

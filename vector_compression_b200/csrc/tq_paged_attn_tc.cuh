@@ -35,11 +35,11 @@
 // 23 (what a float's significand gives without further instructions), three
 // bytes each, of whose nine products the one below 2^-30 is left out: 2e-7 to
 // 5e-7, as fp32 sums.  The third byte of the weights is a tile of its own, laid
-// out as that of the queries.  The case below takes 95 us so, 48 sequences of 0
+// out as that of the queries.  The case below takes 96 us so, 48 sequences of 0
 // to 6000 tokens with 2 x 8 heads 41 us instead of 38.
 //
 // What bounds it (8 sequences of 31 thousand tokens, 8 KV heads of 4 query
-// heads, d = m = 128, 3 bits: 78 us, 2.7 TB/s, of 33 us that the bytes take): the
+// heads, d = m = 128, 3 bits: 79 us, 2.7 TB/s, of 33 us that the bytes take): the
 // ALU (51% busy: masks, permutes) and the tensor pipe (39%), which overlap only
 // in part; with 4, 8 and 12 warps an SM it takes 104, 80 and 78 us.
 #pragma once
@@ -112,6 +112,13 @@ __device__ __forceinline__ void mma_uu(int (&d)[4], uint32_t a0, uint32_t a1, ui
 __device__ __forceinline__ float pow2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// The larger of two numbers, NaN where one is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
 
@@ -405,13 +412,15 @@ __global__ void __launch_bounds__(64, Shape<KK, KV, NT, DP, MQ, FINE>::CTAS)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float* vn = reinterpret_cast<const float*>(vb + i * S::VB + KV * DP);
+        const int ni = __shfl_sync(0xffffffffu, nt, i);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const float p = pow2(x[n][i][r] - base);
-          // the maximum takes NaN to 0: the norm of a slot without a token can be anything
-          const float w = fmaxf(p * vn[16 * th + 4 * (r ^ th) + ts], 0.f);
+          // the norm of a slot without a token can be anything; a token's that is NaN stays one
+          const int t = 16 * th + 4 * (r ^ th) + ts;
+          const float w = t < ni ? max_nan(p * vn[t], 0.f) : 0.f;
           l += p;
-          big = fmaxf(big, w);
+          big = max_nan(big, w);
           if (KV == 4) wsum += w;
           x[n][i][r] = w;
         }
@@ -428,9 +437,10 @@ __global__ void __launch_bounds__(64, Shape<KK, KV, NT, DP, MQ, FINE>::CTAS)
       l_run[n] += l;
       if (KV == 4) w_run[n] += wsum;
 #pragma unroll
-      for (int k = 4; k < 32; k *= 2) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, k));
-      const float inv = big > 1e-33f ? kWeight / big : 0.f;
-      back[n] = big > 1e-33f ? big * ((FINE ? 0x1p24f : 0x1p8f) / kWeight) * K.unit : 0.f;
+      for (int k = 4; k < 32; k *= 2) big = max_nan(big, __shfl_xor_sync(0xffffffffu, big, k));
+      // a weight that is not finite makes all of its head's sums NaN (infinity times 0), whatever its integer is
+      const float inv = big <= 1e-33f ? 0.f : kWeight / big;
+      back[n] = big <= 1e-33f ? 0.f : fmaf(big, 0.f, big * ((FINE ? 0x1p24f : 0x1p8f) / kWeight) * K.unit);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         // the integer part in the low 16 or 23 bits (2^23 itself: 2^7 in byte 2)
