@@ -34,7 +34,6 @@ void check(const char* fn, tq_status status) {
 
 const Tensor* opt(const Maybe& t) { return t ? &*t : nullptr; }
 void* ptr(const Tensor& t) { return t.data_ptr(); }
-void* ptr(const Maybe& t) { return t ? t->data_ptr() : nullptr; }
 
 // The CUDA device that every given tensor is on.
 c10::Device device_of(std::initializer_list<const Tensor*> ts) {
@@ -72,6 +71,12 @@ void* whole(const char* name, const Tensor& t, at::ScalarType type, at::IntArray
 template <typename T>
 T* whole(const char* name, const Tensor& t, at::ScalarType type, at::IntArrayRef shape) {
   return static_cast<T*>(whole(name, t, type, shape));
+}
+
+// The first byte of a workspace, whose bytes lie together (an expanded or strided view holds fewer than it counts).
+void* together(const Tensor& ws) {
+  if (!ws.is_contiguous()) refuse("ws must be contiguous");
+  return ws.data_ptr();
 }
 
 int64_t rows_of(const char* name, const Tensor& t) {
@@ -210,11 +215,12 @@ std::tuple<Tensor, Maybe> paged_attention(const Paged& pg, Tensor q, const Tenso
   const int32_t* n = whole<int32_t>("lens", lens, at::kInt, {B});
   void* o = whole("out", *out, q.scalar_type(), {B, Hq, d});
   float* l = lse ? whole<float>("lse", *lse, at::kFloat, {B, Hq}) : nullptr;
+  void* const w = ws ? together(*ws) : nullptr;
   tq_status e;
   {
     py::gil_scoped_release go;
     e = tq_paged_attention(pg.get(), ptr(q), dt, std::max(q.stride(0), Hq * d), (int)B, (int)Hq, from, pool.size(0), layer,
-                           n, t.p, t.ld, t.width, (float)scale, o, l, ptr(ws), ws ? ws->nbytes() : 0, here.stream);
+                           n, t.p, t.ld, t.width, (float)scale, o, l, w, ws ? ws->nbytes() : 0, here.stream);
   }
   check("tq_paged_attention", e);
   return {*out, want_lse ? lse : std::nullopt};
@@ -255,10 +261,11 @@ Tensor paged_compact(const Paged& pg, const Tensor& pool, const Tensor& tables, 
   const Table t("tables", tables, B), to("tables_out", *tables_out, B);
   const int32_t* l = whole<int32_t>("lens", lens, at::kInt, {B});
   int32_t* const u = whole<int32_t>("n_used", *n_used, at::kInt, {1});
+  void* const w = together(*ws);
   tq_status e;
   {
     py::gil_scoped_release go;
-    e = tq_paged_compact(pg.get(), p, pool.size(0), t.p, to.p, t.ld, t.width, l, (int)B, u, ptr(ws), ws->nbytes(),
+    e = tq_paged_compact(pg.get(), p, pool.size(0), t.p, to.p, t.ld, t.width, l, (int)B, u, w, ws->nbytes(),
                          here.stream);
   }
   check("tq_paged_compact", e);
