@@ -454,6 +454,8 @@ def tq_paged_attention(pg: TQPaged, q, pool, layer: int, lens, tables, scale: fl
     bf16; any stride between sequences), over the first lens[b] (int32 [B])
     tokens of the pages tables[b] of one layer.  Returns out [B, Hq, d], or
     (out, lse [B, Hq]) with want_lse."""
+    if not pg.kp.handle:  # the cache's handle has the sketch's address
+        raise ValueError("the quantizer of the cache's keys is closed")
     fn = _bound().paged_attention
     if stream is not None:
         got = _on_stream(stream, q, fn, pg._c, q, pool, layer, lens, tables, scale, out, lse, ws, want_lse)
