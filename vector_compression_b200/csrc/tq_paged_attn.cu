@@ -442,6 +442,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const AttnArgs A,
   if (lane == 0 && A.lse) A.lse[(int64_t)b * A.Hq + hq] = l == 0.f ? -INFINITY : kLn2 * (top + log2f(l));
 }
 
+// What attention_any_kernel may take of shared memory for the queries of a group (q' and u); its own arrays fit beside it.
+constexpr size_t kAnyQueries = 200 * 1024;
+
 // How a call is run: the tensor-core kernel where it has the shape, else the one for any.
 struct Plan {
   TcShape tc;
@@ -493,8 +496,9 @@ cudaError_t run(const AttnArgs& a, const tq_paged* pg, const Plan& p, cudaStream
     queries_kernel<A32, 0><<<pairs, 512, 0, st>>>(a, pg->kq, 0.f);
     constexpr int NC = A32 > 4 ? 2 : 1;
     const size_t smem = (size_t)a.G * (a.L.dp + pg->kq.m) * sizeof(float);
-    // function attributes are per device: set on every call (a cheap host call)
-    e = cudaFuncSetAttribute(attention_any_kernel<NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // function attributes are per device: set on every call (a cheap host call), always to the same value, since
+    // calls of other threads and shapes share it
+    e = cudaFuncSetAttribute(attention_any_kernel<NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kAnyQueries);
     if (e == cudaSuccess) e = launch_after(attention_any_kernel<NC>, dim3(a.workers), 128, smem, st, a, pg->kq, pg->vq);
   }
   if (e != cudaSuccess) return e;
@@ -504,7 +508,7 @@ cudaError_t run(const AttnArgs& a, const tq_paged* pg, const Plan& p, cudaStream
 }
 
 // What does not fit the kernels' shared memory: the queries of a group.
-bool too_wide(const tq_paged* pg, int G) { return (size_t)G * (pg->lay.dp + pg->kq.m) * sizeof(float) > 200 * 1024; }
+bool too_wide(const tq_paged* pg, int G) { return (size_t)G * (pg->lay.dp + pg->kq.m) * sizeof(float) > kAnyQueries; }
 
 }  // namespace
 }  // namespace paged
