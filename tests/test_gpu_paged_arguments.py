@@ -24,3 +24,20 @@ def test_a_workspace_whose_bytes_do_not_lie_together_is_refused():
         call(byte(n))
         call(byte(4 * n + 512).view(2, -1)[1, : (n + 3) // 4 * 4].view(torch.int32))  # any type, part of another
     tq.tq_sync_check()
+
+
+def test_norm_rope_into_rows_between_one_another():
+    """Heads of one token between those of others, with nothing shared: written as anywhere else."""
+    rope, pos = tq.TQRope(64), torch.arange(5, device=DEV)
+    q = torch.randn(5, 2, 64, device=DEV)
+    want, _ = tq.tq_qk_norm_rope(rope, q, None, pos)
+    for ot, oh in ((128, 64), (64, 320), (128, 5 * 64), (130, 65), (128, 3 * 64 + 128)):
+        buf = torch.full((5 * ot + 2 * oh + 64,), 7.0, device=DEV)
+        out = buf.as_strided((5, 2, 64), (ot, oh, 1))
+        tq.tq_qk_norm_rope(rope, q, None, pos, q_out=out)
+        assert torch.equal(out, want), (ot, oh)
+    for ot, oh in ((64, 64), (64, 128), (128, 100), (100, 350)):
+        buf = torch.full((5 * ot + 2 * oh + 64,), 7.0, device=DEV)
+        with pytest.raises(tq.TQError):
+            tq.tq_qk_norm_rope(rope, q, None, pos, q_out=buf.as_strided((5, 2, 64), (ot, oh, 1)))
+        assert bool((buf == 7).all())

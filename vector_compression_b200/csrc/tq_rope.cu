@@ -387,6 +387,22 @@ bool fits(const Args& a, bool pairs, int esz, int v) {
   return a.d % v == 0 && (a.rot / 2) % v == 0 && (!pairs || a.rot % (2 * v) == 0);
 }
 
+// Whether two of a side's output rows (t yt + h yh, d elements each) share an element.
+bool rows_overlap(const Side& s, int64_t n_tok, int d) {
+  if ((n_tok > 1 && s.yt < d) || (s.heads > 1 && s.yh < d)) return true;
+  if (n_tok == 1 || s.heads == 1) return false;
+  // heads within a token, or tokens within a head (a quotient, since a product could pass 64 bits)
+  if (s.yh <= (s.yt - d) / (s.heads - 1) || s.yt <= (s.yh - d) / (n_tok - 1)) return false;
+  // heads of one token between those of others: row (t, h + j) against (t + i, h), the two i around j yh / yt
+  for (int64_t j = 1; j < s.heads; ++j) {
+    const __int128 at = (__int128)j * s.yh;
+    const __int128 i = at / s.yt;
+    const int64_t past = (int64_t)(at - i * s.yt);
+    if ((i < n_tok && past < d) || (i + 1 < n_tok && s.yt - past < d)) return true;
+  }
+  return false;
+}
+
 }  // namespace rope
 }  // namespace tq
 
@@ -450,7 +466,7 @@ extern "C" tq_status tq_qk_norm_rope(const tq_rope* rope, tq_dtype dt, int64_t n
     if (!s.x || !s.y || reinterpret_cast<uintptr_t>(s.x) % esz || reinterpret_cast<uintptr_t>(s.y) % esz ||
         reinterpret_cast<uintptr_t>(s.w) % esz)
       return TQ_ERR_INVALID_ARG;
-    if (s.xt < 0 || s.xh < 0 || (n_tok > 1 && s.yt < d) || (s.heads > 1 && s.yh < d)) return TQ_ERR_INVALID_ARG;
+    if (s.xt < 0 || s.xh < 0 || rows_overlap(s, n_tok, d)) return TQ_ERR_INVALID_ARG;
   }
   a.pos = pos;
   a.d = d;
