@@ -5,11 +5,13 @@
 The shared library is written next to this file so that it travels with the
 source tree, and with it _torch_binding.so, the calls on torch tensors that run
 once per layer and step; both are rebuilt when any source under csrc/, binding/ or
-include/ is newer.
+include/ is newer.  Without torch the library alone is built, which a user of the
+C ABI needs nothing but nvcc and its host compiler for.
 """
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import subprocess
 import sys
@@ -40,11 +42,16 @@ def deps():
         glob.glob(os.path.join(ROOT, "include", "*.h"))
 
 
+def has_torch() -> bool:
+    return importlib.util.find_spec("torch") is not None
+
+
 def needs_build() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
+    built, of = ([LIB, BINDING], deps() + [BINDING_SRC]) if has_torch() else ([LIB], deps())
+    if not all(os.path.exists(f) for f in built):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
-    return any(os.path.getmtime(f) > t for f in deps() + [BINDING_SRC])
+    t = min(os.path.getmtime(f) for f in built)
+    return any(os.path.getmtime(f) > t for f in of)
 
 
 def binding_commands(obj: str, out: str):
@@ -80,9 +87,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
     t0 = time.time()
     procs = []
     objs = []
-    binding_obj = os.path.join(objdir, "tq_torch.cpp.o")
-    compile_binding, link_binding = binding_commands(binding_obj, BINDING + ".tmp")
-    procs.append((compile_binding, subprocess.Popen(compile_binding, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
+    link_binding = None
+    if has_torch():
+        compile_binding, link_binding = binding_commands(os.path.join(objdir, "tq_torch.cpp.o"), BINDING + ".tmp")
+        procs.append((compile_binding, subprocess.Popen(compile_binding, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     for src in sources():
         obj = os.path.join(objdir, os.path.basename(src) + ".o")
         objs.append(obj)
@@ -94,7 +102,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         out, _ = p.communicate()
         if p.returncode != 0:
             sys.stderr.write(out.decode(errors="replace"))
-            raise RuntimeError("nvcc failed: " + " ".join(cmd))
+            raise RuntimeError("compilation failed: " + " ".join(cmd))
         if verbose and out:
             sys.stderr.write(out.decode(errors="replace"))
     tmp = LIB + ".tmp"
@@ -102,10 +110,11 @@ def build(force: bool = False, verbose: bool = False) -> str:
             "-lcudart"]
     subprocess.run(link, check=True)
     os.replace(tmp, LIB)
-    subprocess.run(link_binding, check=True)
-    os.replace(BINDING + ".tmp", BINDING)
+    if link_binding:
+        subprocess.run(link_binding, check=True)
+        os.replace(BINDING + ".tmp", BINDING)
     if verbose:
-        print(f"built {LIB} in {time.time() - t0:.1f}s")
+        print(f"built {LIB} in {time.time() - t0:.1f}s" + ("" if link_binding else " (no torch: without its binding)"))
     return LIB
 
 
