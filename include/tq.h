@@ -453,9 +453,9 @@ tq_status tq_paged_info(const tq_paged* pg, int* block_words, int64_t* page_word
 /*
  * tq_paged_append -- write encoded tokens into the pages of one layer.  The
  * rows are the encoders' ROW outputs for vectors [n_tok][Hkv] (kcodes, ksigns,
- * knorms, krnorms of tq_encode_prod; vcodes, vnorms of tq_encode_mse), the new
- * tokens of sequence b being rows cu[b] .. cu[b + 1] - 1, written to
- * positions start[b], start[b] + 1, ...
+ * knorms, krnorms of tq_encode_prod; vcodes, vnorms of tq_encode_mse), from any
+ * token of them on, the new tokens of sequence b being rows cu[b] .. cu[b + 1] -
+ * 1, written to positions start[b], start[b] + 1, ...
  *   cu      DEVICE int32 [B + 1], ascending, 0 <= cu[0], cu[B] <= n_tok; rows
  *           outside [cu[0], cu[B]) are ignored.  NULL: one token per sequence
  *           (n_tok = B)

@@ -14,7 +14,7 @@ namespace tq {
 namespace paged {
 namespace {
 
-inline bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 inline bool al256(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
 
 // ---------------------------------------------------------------- append
@@ -584,7 +584,10 @@ extern "C" tq_status tq_paged_append(const tq_paged* pg, uint32_t* pool, int64_t
   if (bad_pool(L, pool, n_pages) || bad_table(L, tables, table_ld, max_pages)) return TQ_ERR_INVALID_ARG;
   if (!kcodes || !ksigns || !knorms || !krnorms || !vcodes || !vnorms || !start || mis4(start) || mis4(cu))
     return TQ_ERR_INVALID_ARG;
-  if (!al16(kcodes) || !al16(ksigns) || !al16(knorms) || !al16(krnorms) || !al16(vcodes) || !al16(vnorms))
+  // key words are read in granules where those lie in one row each, the others one by one: any row can be the first
+  const uintptr_t unit = L.kw % L.gr == 0 ? 4 * L.gr : 4;
+  if (!aligned(kcodes, unit) || !aligned(ksigns, unit) || !aligned(vcodes, 4) || !aligned(knorms, 4) ||
+      !aligned(vnorms, 4) || !aligned(krnorms, L.r16 ? 2 : 4))
     return TQ_ERR_INVALID_ARG;
   // A step's tokens are a run each, and wait for no other: a warp each.  Of prompts a warp looks through 32, in which
   // one block begins; of shorter sequences through 8, of which several can begin a run.
