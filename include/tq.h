@@ -484,7 +484,8 @@ tq_status tq_paged_append(const tq_paged* pg, uint32_t* pool, int64_t n_pages, i
  *           with no token are 0
  *   lse     DEVICE float [B][Hq] or NULL: log(sum(exp(scale * s))), -inf
  *           where there is no token; joins the result with attention over
- *           tokens that are not in the cache
+ *           tokens that are not in the cache.  A score of -inf (an infinite key
+ *           norm) is a token that takes no part
  *   ws      tq_paged_attention_workspace_size bytes (for the current device),
  *           256-byte aligned, nothing kept in it between calls: calls that overlap on the GPU
  *           need one each

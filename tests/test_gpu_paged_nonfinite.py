@@ -54,3 +54,41 @@ def test_norms_that_are_not_finite(shape, dtype):
                 # the softmax does not know of the values
                 assert torch.equal(lse, clean_lse) if part == "vn" else bool(torch.isnan(lse[mine]).all())
     tq.tq_sync_check()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_scores_of_minus_infinity_take_no_part(shape, dtype):
+    """Tokens with an infinite key norm: where the sign makes their score -inf, they count as if they were not there,
+    at a sequence's start and where nothing else is left too."""
+    d, bits, vbits, m, r16, G = shape
+    kp, vp, _, _ = quantizers(d, bits, m, vbits, r16)
+    pg, model = tq.TQPaged(kp, vp, 1, 1, 32), Model(kp, vp, 1, 1, 32)
+    rng = np.random.default_rng(d + G + 1)
+    pool, tables = random_cache(rng, model, [200, 40], 7, 0)
+    # one query for all heads, and all of the keys' codes and signs alike: the same sign of score everywhere
+    q = torch.from_numpy(np.repeat(rng.standard_normal((2, 1, d)), G, 1)).to(DEV).to(dtype)
+    for b in range(2):
+        for t in range(224):
+            if 0 <= tables[b, t // 32]:
+                rec = model.record(pool, tables[b, t // 32], 0, 0, 0)
+                for w in range(model.nk):
+                    rec[model.key_place(t % 32, w)] = 0x5a3c96f0 * (w + 1) & 0xffffffff
+
+    def call(pool, lens, t, scale):
+        return tq.tq_paged_attention(pg, q, i32(pool), 0, ints(lens), ints(t), scale, want_lse=True)
+
+    scale = 0.1
+    if float(call(pool, [200, 40], tables, scale)[1][0, 0]) > float(call(pool, [200, 40], tables, -scale)[1][0, 0]):
+        scale = -scale  # scores below zero in sequence 0
+    inf = pool.copy()
+    for t in range(32):  # the first page of sequence 0
+        model.record(inf, tables[0, 0], 0, 0, 0).view(np.float32)[model.kn + t] = np.inf
+    holes = tables.copy()
+    holes[0, 0] = -1
+    got, want = call(inf, [200, 40], tables, scale), call(pool, [200, 40], holes, scale)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    out, lse = call(inf, [32, 40], tables, scale)  # nothing else
+    assert bool((out[0] == 0).all()) and bool(torch.isneginf(lse[0]).all())
+    assert torch.equal(out[1], want[0][1])
+    tq.tq_sync_check()

@@ -327,8 +327,9 @@ __global__ void __launch_bounds__(128) attention_any_kernel(const AttnArgs A, co
         if (g < G) {
           const float x = valid ? A.scale2 * (kn * (am[hh] + kr * aq[hh])) : -INFINITY;
           const float old = m_s[g], top = fmaxf(old, warp_max(x));
-          const float p = valid ? exp2f(x - top) : 0.f;
-          const float corr = exp2f(old - top);
+          const float base = top == -INFINITY ? 0.f : top;  // scores of -inf have no weight, the first ones neither
+          const float p = valid ? exp2f(x - base) : 0.f;
+          const float corr = exp2f(old - base);
           const float sum = warp_sum(p);
           p_s[lane][g] = p * vn;
           if (lane == 0) {
