@@ -379,8 +379,8 @@ tq_status tq_rope_destroy(tq_rope* r); /* NULL is a no-op */
  * projection and this library's encoders and attention, in one pass over
  * both: per head an RMS norm, x / sqrt(mean(x^2) + eps) * w, then the
  * rotation of `rope`.  Sums and rotation in fp32, one rounding at the end.
- * The angle pos * f is reduced to a fraction of a turn exactly (64-bit fixed
- * point), so far positions lose nothing.
+ * The angle pos * f is reduced to a fraction of a turn in 64-bit fixed point,
+ * which is off by pos 2^-63 of a turn.
  *   rope    NULL: no rotation
  *   x       q and k each: DEVICE, n_tok x H heads of d elements of dtype dt,
  *           element strides q_tok / q_head (k_tok / k_head) between tokens and

@@ -5,8 +5,10 @@
 // of the first `rot` coordinates becomes (a cos - b sin, b cos + a sin) with
 // the angle pos f_i.  An angle is needed as a fraction of a turn, so f_i is
 // kept as F_i = f_i / (2 pi) 2^64 and the fraction is the product pos F_i
-// modulo 2^64: one integer multiplication, exact but for F_i's own rounding
-// (pos 2^-65 of a turn).
+// modulo 2^64: one integer multiplication, exact but for what F_i is off by.
+// That is below 2 (its rounding, and f_i made in extended precision, of 2^-63),
+// so the fraction is off by pos 2^-63 of a turn; f_i made in double would make
+// that pos 2^-57.
 //
 // The work is memory: each element is read and written once.  A group of lanes
 // owns a row, each lane holding matching vectors of both halves of the pairs,
@@ -424,17 +426,19 @@ extern "C" tq_status tq_rope_create(int rot, int interleaved, double base, tq_ro
   const double two_pi = 2.0 * M_PI;
   // the pair number at which a pair makes `turns` turns over orig_len
   auto pair_of = [&](double turns) { return rot * std::log(orig_len / (turns * two_pi)) / (2.0 * std::log(base)); };
+  using real = long double;
   for (int i = 0; i < rot / 2; ++i) {
-    double f = std::pow(base, -2.0 * i / rot), keep = 1.0;  // keep: the share of f that is not slowed down
-    if (scaling == TQ_ROPE_LINEAR) keep = 0.0;
-    if (scaling == TQ_ROPE_BANDS) keep = std::fmin(1.0, std::fmax(0.0, (orig_len * f / two_pi - low) / (high - low)));
+    real f = std::pow((real)base, (real)(-2 * i) / rot), keep = 1;  // keep: the share of f that is not slowed down
+    if (scaling == TQ_ROPE_LINEAR) keep = 0;
+    if (scaling == TQ_ROPE_BANDS)
+      keep = std::fmin((real)1, std::fmax((real)0, (orig_len * f / (2 * M_PIl) - low) / ((real)high - low)));
     if (scaling == TQ_ROPE_YARN) {
       const double first = std::fmax(std::floor(pair_of(high)), 0.0);
       const double last = std::fmin(std::ceil(pair_of(low)), rot - 1.0);
-      keep = 1.0 - std::fmin(1.0, std::fmax(0.0, (i - first) / std::fmax(last - first, 1e-3)));
+      keep = 1 - std::fmin((real)1, std::fmax((real)0, (i - (real)first) / std::fmax(last - first, 1e-3)));
     }
-    if (scaling != TQ_ROPE_PLAIN) f = f * keep + f / factor * (1.0 - keep);
-    r->turn[i] = (uint64_t)((long double)f / (2.0L * M_PIl) * 0x1p64L + 0.5L);
+    if (scaling != TQ_ROPE_PLAIN) f = f * keep + f / factor * (1 - keep);
+    r->turn[i] = (uint64_t)(f / (2 * M_PIl) * 0x1p64L + 0.5L);
   }
   *out = r;
   return TQ_OK;
