@@ -42,3 +42,21 @@ def test_norm_rope_into_rows_between_one_another():
         with pytest.raises(tq.TQError):
             tq.tq_qk_norm_rope(rope, q, None, pos, q_out=buf.as_strided((5, 2, 64), (ot, oh, 1)))
         assert bool((buf == 7).all())
+
+
+def test_sizes_beyond_32_bits_are_refused():
+    """Not taken modulo 2^32: heads of 2^32 + 64 elements are no heads of 64."""
+    q = torch.empty(1, 1, (1 << 32) + 64, dtype=torch.float16, device=DEV)
+    with pytest.raises(ValueError, match="too large"):
+        tq.tq_qk_norm_rope(None, q, None)
+    q = torch.ones(1, 1, 64, device=DEV)
+    with pytest.raises(ValueError, match="too large"):
+        tq.tq_qk_norm_rope(None, q.expand(1, (1 << 32) + 1, 64), None, q_out=q.expand(1, (1 << 32) + 1, 64))
+    kp, vp, _, _ = quantizers(64, 3)
+    pg = tq.TQPaged(kp, vp, 1, 1, 32)
+    pool, tables, lens = pg.new_pool(1), ints([[0]]), ints([1])
+    with pytest.raises(ValueError, match="too large"):
+        tq.tq_paged_attention(pg, q.expand(1, (1 << 32) + 1, 64), pool, 0, lens, tables, 1.0)
+    with pytest.raises(ValueError, match="too large"):
+        tq.tq_paged_fork(pg, pool, tables, lens, *[ints([0]).expand((1 << 32) + 1)] * 3)
+    assert bool((q == 1).all()) and bool((pool == 0).all())

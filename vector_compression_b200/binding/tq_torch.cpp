@@ -32,6 +32,12 @@ void check(const char* fn, tq_status status) {
   throw py::error_already_set();
 }
 
+// A size as the library takes it.
+int count(const char* what, int64_t n) {
+  if (n > 0x7fffffff) refuse(std::string(what) + " is too large");
+  return (int)n;
+}
+
 const Tensor* opt(const Maybe& t) { return t ? &*t : nullptr; }
 void* ptr(const Tensor& t) { return t.data_ptr(); }
 
@@ -102,7 +108,7 @@ struct Heads {
 std::tuple<Tensor, Maybe> qk_norm_rope(uintptr_t rope, const Tensor& q, const Maybe& k, const Maybe& pos, const Maybe& wq,
                                        const Maybe& wk, double eps, Maybe q_out, Maybe k_out) {
   if (q.dim() != 3) refuse("q must have three dimensions");
-  const int64_t n = q.size(0), Hq = q.size(1), d = q.size(2);
+  const int64_t n = q.size(0), Hq = count("the number of heads", q.size(1)), d = count("the size of a head", q.size(2));
   const at::ScalarType type = q.scalar_type();
   const tq_dtype dt = dtype_of("q", q);
   const Here here(device_of({&q, opt(k), opt(pos), opt(wq), opt(wk), opt(q_out), opt(k_out)}));
@@ -114,7 +120,7 @@ std::tuple<Tensor, Maybe> qk_norm_rope(uintptr_t rope, const Tensor& q, const Ma
   Heads ki = qi, ko = qo;
   if (k) {
     if (k->dim() != 3) refuse("k must have three dimensions");
-    Hkv = k->size(1);
+    Hkv = count("the number of heads", k->size(1));
     ki = Heads("k", *k, n, Hkv, d, type);
     if (!k_out) k_out = at::empty(k->sizes(), k->options());
     ko = Heads("k_out", *k_out, n, Hkv, d, type);
@@ -154,8 +160,7 @@ struct Table {
   Table(const char* name, const Tensor& t, int64_t B) {
     if (t.scalar_type() != at::kInt || t.dim() != 2 || t.size(0) != B)
       refuse(std::string(name) + " must be int32 [" + std::to_string(B) + ", max_pages]");
-    if (t.size(1) > 0x7fffffff) refuse(std::string(name) + " is too wide");
-    width = (int)t.size(1);
+    width = count("the number of pages of a sequence", t.size(1));
     if (B && ((t.stride(1) != 1 && width > 1) || (B > 1 && t.stride(0) < width)))
       refuse("the rows of " + std::string(name) + " must be contiguous and apart");
     p = static_cast<int32_t*>(t.data_ptr());
@@ -173,7 +178,7 @@ T* encoded(const char* name, const Tensor& t, at::ScalarType type, int64_t n) {
 void paged_append(const Paged& pg, const Tensor& pool, int layer, const Tensor& kcodes, const Tensor& ksigns,
                   const Tensor& knorms, const Tensor& krnorms, const Tensor& vcodes, const Tensor& vnorms,
                   const Tensor& start, const Tensor& tables, const Maybe& cu) {
-  const int64_t B = rows_of("start", start), rows = knorms.numel(), n_tok = rows / pg.hkv;
+  const int64_t B = count("the number of sequences", rows_of("start", start)), rows = knorms.numel(), n_tok = rows / pg.hkv;
   if (rows != n_tok * pg.hkv) refuse(std::to_string(rows) + " rows are no multiple of " + std::to_string(pg.hkv) + " heads");
   if (!cu && n_tok != B) refuse(std::to_string(n_tok) + " tokens for " + std::to_string(B) + " sequences need cu");
   const Here here(device_of({&pool, &kcodes, &ksigns, &knorms, &krnorms, &vcodes, &vnorms, &start, &tables, opt(cu)}));
@@ -199,7 +204,7 @@ void paged_append(const Paged& pg, const Tensor& pool, int layer, const Tensor& 
 std::tuple<Tensor, Maybe> paged_attention(const Paged& pg, Tensor q, const Tensor& pool, int layer, const Tensor& lens,
                                           const Tensor& tables, double scale, Maybe out, Maybe lse, Maybe ws, bool want_lse) {
   if (q.dim() != 3 || q.size(2) != pg.d) refuse("q must be [B, Hq, " + std::to_string(pg.d) + "]");
-  const int64_t B = q.size(0), Hq = q.size(1), d = q.size(2);
+  const int64_t B = count("the number of sequences", q.size(0)), Hq = count("the number of heads", q.size(1)), d = q.size(2);
   const tq_dtype dt = dtype_of("q", q);
   const Here here(device_of({&q, &pool, &lens, &tables, opt(out), opt(lse), opt(ws)}));
   if (q.numel() && (q.stride(2) != 1 || q.stride(1) != d || (B > 1 && q.stride(0) < Hq * d))) q = q.contiguous();
@@ -228,7 +233,7 @@ std::tuple<Tensor, Maybe> paged_attention(const Paged& pg, Tensor q, const Tenso
 
 void paged_fork(const Paged& pg, const Tensor& pool, const Tensor& tables, const Tensor& lens, const Tensor& parents,
                 const Tensor& children, const Tensor& fresh) {
-  const int64_t B = rows_of("lens", lens), n = rows_of("parents", parents);
+  const int64_t B = count("the number of sequences", rows_of("lens", lens)), n = count("the number of forks", rows_of("parents", parents));
   const Here here(device_of({&pool, &tables, &lens, &parents, &children, &fresh}));
   const Table t("tables", tables, B);
   uint32_t* const p = pg.pool(pool);
@@ -246,7 +251,7 @@ void paged_fork(const Paged& pg, const Tensor& pool, const Tensor& tables, const
 
 Tensor paged_compact(const Paged& pg, const Tensor& pool, const Tensor& tables, const Tensor& lens, Maybe tables_out,
                      Maybe n_used, Maybe ws) {
-  const int64_t B = rows_of("lens", lens);
+  const int64_t B = count("the number of sequences", rows_of("lens", lens));
   const Here here(device_of({&pool, &tables, &lens, opt(tables_out), opt(n_used), opt(ws)}));
   if (!tables_out) tables_out = tables;
   else if (tables_out->sizes() != tables.sizes() || tables_out->strides() != tables.strides())
