@@ -46,3 +46,26 @@ def test_key_words_that_begin_inside_a_granule_are_refused():
         with pytest.raises(tq.TQError):
             tq.tq_paged_append(pg, pool, 0, part, (vals[0].reshape(-1)[:12], vals[1][:1]), ints([0]), tables)
     assert bool((pool == 0).all())
+
+
+@pytest.mark.parametrize("B,most", [(33, 3), (64, 90), (1025, 2), (2100, 40)])
+def test_more_sequences_than_a_warp_holds(B, most):
+    """With cu, a token's sequence is searched among more than 32: empty ones at both ends and between, tokens of no
+    sequence before and behind."""
+    kp, vp, _, _ = quantizers(64, 2, 32)
+    pg, model = tq.TQPaged(kp, vp, 1, 1, 32), Model(kp, vp, 1, 1, 32)
+    rng = np.random.default_rng(B)
+    new = rng.integers(0, most + 1, B) * rng.integers(0, 2, B)
+    new[[0, 1, -2, -1]] = 0
+    new[[2, 31, 32, B // 2]] = most  # at the borders of the search's steps
+    cu = 5 + np.concatenate([[0], np.cumsum(new)])
+    n, width = int(cu[-1]) + 4, -(-(most + 40) // 32)
+    start = rng.integers(0, 40, B)
+    tables = rng.permutation(B * width).reshape(B, width).astype(np.int32)
+    pool = rng.integers(0, 1 << 32, (B * width, model.page_words), dtype=np.uint64).astype(np.uint32)
+    ref, keys, vals = rows(rng, n, 1, model)
+    got = i32(pool)
+    tq.tq_paged_append(pg, got, 0, keys, vals, ints(start), ints(tables), cu=ints(cu))
+    model.append(pool, 0, *ref, cu, start, tables)
+    assert np.array_equal(u32(got), pool)
+    tq.tq_sync_check()

@@ -60,3 +60,15 @@ def test_sizes_beyond_32_bits_are_refused():
     with pytest.raises(ValueError, match="too large"):
         tq.tq_paged_fork(pg, pool, tables, lens, *[ints([0]).expand((1 << 32) + 1)] * 3)
     assert bool((q == 1).all()) and bool((pool == 0).all())
+
+
+def test_the_sizes_of_a_cache():
+    """Of handles that are otherwise right: the largest sizes are taken, the next ones refused."""
+    kp, vp, _, _ = quantizers(128, 3)
+    for layers, hkv, page in ((4096, 1, 32), (1, 1024, 32), (1, 1, 65536), (1, 1, 96)):
+        pg = tq.TQPaged(kp, vp, layers, hkv, page)
+        assert pg.page_words == layers * hkv * page // 32 * pg.block_words
+    for layers, hkv, page in ((0, 1, 32), (-1, 1, 32), (1, 0, 32), (1, 1, 31), (1, 1, 0), (1, 1, 48), (4097, 1, 32),
+                              (1, 1025, 32), (1, 1, 65536 + 32)):
+        with pytest.raises(tq.TQError):
+            tq.TQPaged(kp, vp, layers, hkv, page)
