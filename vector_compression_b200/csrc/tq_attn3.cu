@@ -458,14 +458,17 @@ __global__ void __launch_bounds__(DPT) attn_kernel(Params P) {
           const float w = p * vn;
           sc[hh] = w;
           lpart[h] += p;
-          wmax[h] = fmaxf(wmax[h], w);
+          wmax[h] = max_nan(wmax[h], w);  // a norm that is NaN goes on
         }
         *reinterpret_cast<float4*>(&s_score[t][h4]) = sc4;
       }
     }
 #pragma unroll
     for (int h = 0; h < HN; ++h) {
-      const float a = warp_sum(lpart[h]), b = warp_max(wmax[h]);
+      const float a = warp_sum(lpart[h]);
+      float b = wmax[h];
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) b = max_nan(b, __shfl_xor_sync(0xffffffffu, b, o));
       if (lane == 0) {
         s_red[1][warp][h] = a;
         s_red[2][warp][h] = b;
@@ -478,8 +481,9 @@ __global__ void __launch_bounds__(DPT) attn_kernel(Params P) {
     for (int h = 0; h < HN; ++h) {
       float mx = 0.f;
 #pragma unroll
-      for (int v = 0; v < kWarps; ++v) mx = fmaxf(mx, s_red[2][v][h]);
-      winv[h] = mx > 0.f ? 65535.0f / mx : 0.f;
+      for (int v = 0; v < kWarps; ++v) mx = max_nan(mx, s_red[2][v][h]);
+      // a weight that is not finite makes the head's sums NaN (infinity times 0), whatever its integer is
+      winv[h] = mx > 0.f ? fmaf(mx, 0.f, 65535.0f / mx) : mx;
     }
     int wsum[HN];
 #pragma unroll
@@ -530,7 +534,7 @@ __global__ void __launch_bounds__(DPT) attn_kernel(Params P) {
       }
       const float mold = s_head[h][4];
       corr[nt] = mold == -INFINITY ? 0.f : exp2f(mold - mn);
-      wscale[nt] = wi > 0.f ? 1.0f / wi : 0.f;
+      wscale[nt] = wi > 0.f ? 1.0f / wi : wi;
       int ws = 0;
 #pragma unroll
       for (int v = 0; v < kWarps; ++v) ws += __float_as_int(s_red[0][v][h]);

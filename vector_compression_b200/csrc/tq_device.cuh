@@ -43,6 +43,13 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
+// The larger of two numbers, NaN where one is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // Unnormalized Walsh-Hadamard transform (Sylvester / natural order) of a
 // vector of 32*A values spread over a warp: lane l holds coordinates 32a + l
 // in v[a].  Cross-lane stages (h = 1..16) use shuffles; stages h = 32, 64, ...

@@ -115,13 +115,6 @@ __device__ __forceinline__ float pow2(float x) {
   return r;
 }
 
-// The larger of two numbers, NaN where one is.
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-
 // Place of word base + wt of token 0 in the staged key words, wt in [0, 4); a token is GR words further.
 template <int GR>
 __device__ __forceinline__ int word_place(int base, int wt) {
