@@ -92,3 +92,28 @@ def test_scores_of_minus_infinity_take_no_part(shape, dtype):
     assert bool((out[0] == 0).all()) and bool(torch.isneginf(lse[0]).all())
     assert torch.equal(out[1], want[0][1])
     tq.tq_sync_check()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("size", [1e-30, 3e-32, 9e-33, 2e-34, 1e-40, 0.0])
+def test_value_norms_near_the_smallest_numbers(size, dtype):
+    """Weights are divided by their largest: of ones below 1e-31 nothing has to be left, but nothing else may come.
+    Beside them in one batch, ordinary norms with one tiny group, and with a tiny tail of the softmax."""
+    kp, vp, kq, vq = quantizers(128, 3)
+    pg, model = tq.TQPaged(kp, vp, 1, 1, 32), Model(kp, vp, 1, 1, 32)
+    rng = np.random.default_rng(33)
+    lens = [300, 300, 300]
+    pool, tables = random_cache(rng, model, lens, 10, 0)
+    for b, t0, t1 in ((0, 0, 300), (1, 128, 256)):
+        for t in range(t0, t1):
+            f = model.record(pool, tables[b, t // 32], 0, 0, 0).view(np.float32)
+            f[model.vn + t % 32] *= np.float32(size)
+    q = torch.from_numpy(rng.standard_normal((3, 4, 128))).to(DEV).to(dtype)
+    q[2] *= 30
+    got, lse = tq.tq_paged_attention(pg, q, i32(pool), 0, ints(lens), ints(tables), 0.088, want_lse=True)
+    out, want, spread, delta = model.attention(pool, 0, kq, vq, q.double().cpu().numpy(), lens, tables, 0.088)
+    # as tests/test_gpu_paged.py, and what is taken to 0: weights of 1e-31 (the softmax's sum is 1 or more), or all
+    eps = 2.0 ** -24 if dtype == torch.float32 else 2.0 ** -8
+    tol = eps * abs(out) + ((2 * delta + 2.0 ** -15) * spread)[..., None] + np.minimum(spread, 300 * 1e-31)[..., None]
+    assert np.all(abs(got.double().cpu().numpy() - out) <= tol)
+    assert np.all(abs(lse.double().cpu().numpy() - want) <= delta + 8 * 2.0 ** -24 * abs(want) + 2.0 ** -22)

@@ -147,6 +147,7 @@ __global__ void __launch_bounds__(64, Shape<KK, KV, NT, DP, MQ, FINE>::CTAS)
   using S = Shape<KK, KV, NT, DP, MQ, FINE>;
   constexpr int WPP = S::WPP, SW = S::SW, NQ = S::NQ, FK = S::FK, STEPS = S::STEPS, WT = S::WT;
   constexpr float kWeight = FINE ? 8388607.f : 65535.f;  // the largest weight of a group
+  constexpr float kNone = FINE ? 1e-31f : 1e-33f;  // weights up to this count as 0: kWeight divided by more is finite
   extern __shared__ __align__(128) unsigned char smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, tig = lane & 3;
@@ -432,8 +433,8 @@ __global__ void __launch_bounds__(64, Shape<KK, KV, NT, DP, MQ, FINE>::CTAS)
 #pragma unroll
       for (int k = 4; k < 32; k *= 2) big = max_nan(big, __shfl_xor_sync(0xffffffffu, big, k));
       // a weight that is not finite makes all of its head's sums NaN (infinity times 0), whatever its integer is
-      const float inv = big <= 1e-33f ? 0.f : kWeight / big;
-      back[n] = big <= 1e-33f ? 0.f : fmaf(big, 0.f, big * ((FINE ? 0x1p24f : 0x1p8f) / kWeight) * K.unit);
+      const float inv = big <= kNone ? 0.f : kWeight / big;
+      back[n] = big <= kNone ? 0.f : fmaf(big, 0.f, big * ((FINE ? 0x1p24f : 0x1p8f) / kWeight) * K.unit);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         // the integer part in the low 16 or 23 bits (2^23 itself: 2^7 in byte 2)
