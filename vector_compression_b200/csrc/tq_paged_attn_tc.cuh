@@ -35,12 +35,12 @@
 // 23 (what a float's significand gives without further instructions), three
 // bytes each, of whose nine products the one below 2^-30 is left out: 2e-7 to
 // 5e-7, as fp32 sums.  The third byte of the weights is a tile of its own, laid
-// out as that of the queries.  The case below takes 96 us so, 48 sequences of 0
-// to 6000 tokens with 2 x 8 heads 41 us instead of 38.
+// out as that of the queries.  A call of the case below takes 97 us so instead of
+// 85, one of 48 sequences of 0 to 6000 tokens with 2 x 8 heads 41 instead of 38.
 //
 // What bounds it (8 sequences of 31 thousand tokens, 8 KV heads of 4 query
 // heads, d = m = 128, 3 bits: 79 us, 2.7 TB/s, of 33 us that the bytes take): the
-// ALU (51% busy: masks, permutes) and the tensor pipe (39%), which overlap only
+// ALU (52% busy: masks, permutes) and the tensor pipe (39%), which overlap only
 // in part; with 4, 8 and 12 warps an SM it takes 104, 80 and 78 us.
 #pragma once
 
