@@ -492,7 +492,7 @@ tq_status tq_paged_append(const tq_paged* pg, uint32_t* pool, int64_t n_pages, i
  * With key codes of 1..3 bits and (d_pad, m) of (64, 64), (128, 64), (128,
  * 128) or (256, 256) the contractions are exact integer products on the
  * tensor cores: the queries in fixed point (2^-21 of a head's largest entry),
- * value levels and weights in 16 bits where dt is a 16-bit type (5e-5 of an
+ * value levels and weights in 16 bits where dt is a 16-bit type (6e-5 of an
  * output's 2-norm, before it is rounded) and in 23 or more for fp32 (5e-7, as
  * sums in fp32; up to a seventh slower on long contexts); other shapes take a
  * slower kernel in fp32.
