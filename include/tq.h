@@ -494,8 +494,8 @@ tq_status tq_paged_append(const tq_paged* pg, uint32_t* pool, int64_t n_pages, i
  * tensor cores: the queries in fixed point (2^-21 of a head's largest entry),
  * value levels and weights in 16 bits where dt is a 16-bit type (6e-5 of an
  * output's 2-norm, before it is rounded) and in 23 or more for fp32 (5e-7, as
- * sums in fp32; up to a seventh slower on long contexts); other shapes take a
- * slower kernel in fp32.
+ * sums in fp32; 3 to 25 percent slower than 16-bit types, up to a third at d_pad
+ * 256); other shapes take a slower kernel in fp32.
  */
 tq_status tq_paged_attention(const tq_paged* pg, const void* q, tq_dtype dt, int64_t q_ld, int B,
                              int Hq, const uint32_t* pool, int64_t n_pages, int layer,

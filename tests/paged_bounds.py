@@ -7,7 +7,7 @@ allowed.
 
 Score of a token, in units of scale n (n its key norm), per query head:
   - fixed point: entry j of q' is off by at most half of 2^(j mod 4) s, s =
-    max|q'| / 8323072, uniformly: variance s^2 4^(j mod 4) / 12 times C_j^2;
+    max|q'| / (127 2^16), uniformly: variance s^2 4^(j mod 4) / 12 times C_j^2;
     the entries of u in the same way, times (kappa rho)^2;
   - fp32: the rotation adds log2(d_pad) times, u's sums and the score's last
     steps round a dozen times values of the size of rms(q') (the products with
@@ -26,7 +26,7 @@ Output, 2-norm over a head, R = sqrt(sum p^2 |v|^2) (about |out| for random code
   - the output's rounding, half a step of its type."""
 import numpy as np
 
-Q_MAX = 8323072.0
+Q_MAX = 127.0 * 2 ** 16
 FINE, COARSE = (8388607.0, 8388607.0), (65535.0, 32767.0)
 
 
